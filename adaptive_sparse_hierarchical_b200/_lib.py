@@ -13,6 +13,7 @@ import re
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdash_b200.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "dash.h")
+CACHE_HEADER = os.path.join(os.path.dirname(HERE), "include", "dash_cache.h")
 
 DASH_OK, DASH_EINVAL, DASH_EUNSUPPORTED, DASH_EWORKSPACE, DASH_EALIGN, DASH_ELAUNCH = 0, -1, -2, -3, -4, -5
 DASH_F32, DASH_BF16 = 0, 1
@@ -38,6 +39,31 @@ class dash_paged_kv(ctypes.Structure):
     _fields_ = [("page_table", ctypes.c_void_p), ("max_pages", ctypes.c_int), ("page_size", ctypes.c_int),
                 ("num_pages", ctypes.c_int), ("k_page_stride", ctypes.c_longlong),
                 ("v_page_stride", ctypes.c_longlong)]
+
+
+class dash_q4_kv(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("k_code_page", ctypes.c_longlong), ("k_scale_page", ctypes.c_longlong),
+                ("v_code_page", ctypes.c_longlong), ("v_scale_page", ctypes.c_longlong),
+                ("page_table", ctypes.c_void_p), ("max_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("k_exp", ctypes.c_int), ("v_exp", ctypes.c_int)]
+
+
+class dash_page_array(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_bytes", ctypes.c_longlong), ("page_stride", ctypes.c_longlong)]
+
+
+class dash_row_array(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong),
+                ("unit_bytes", ctypes.c_longlong), ("heads", ctypes.c_int), ("max_units", ctypes.c_int),
+                ("unit_tokens", ctypes.c_int), ("clear", ctypes.c_int)]
+
+
+class dash_pages(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("max_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("page_table", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("seqlens", ctypes.c_void_p), ("arrays", ctypes.POINTER(dash_page_array)),
+                ("rows", ctypes.POINTER(dash_row_array)), ("num_arrays", ctypes.c_int), ("num_rows", ctypes.c_int)]
 
 
 class DashError(RuntimeError):
@@ -84,6 +110,22 @@ def load():
         lib.dash_decode_paged.restype = ctypes.c_int
         lib.dash_backward.argtypes = [P, vp, vp, vp, vp, vp, vp, R, vp, vp, vp, vp, vp, sz, vp]
         lib.dash_backward.restype = ctypes.c_int
+        Q, G, i = ctypes.POINTER(dash_q4_kv), ctypes.POINTER(dash_pages), ctypes.c_int
+        lib.dash_q4_workspace_size.argtypes = [P]
+        lib.dash_q4_workspace_size.restype = sz
+        lib.dash_append_q4.argtypes = [P, Q, vp, vp, i, vp, vp, vp, vp, vp, vp]
+        lib.dash_load_q4.argtypes = [P, Q, vp, i, i, vp, vp, vp, vp]
+        lib.dash_decode_q4.argtypes = [P, Q, vp, vp, vp, vp, R, vp, sz, vp]
+        lib.dash_pages_workspace_size.argtypes = [G]
+        lib.dash_pages_workspace_size.restype = sz
+        lib.dash_pages_copy.argtypes = [G, vp, vp, i, vp, vp, sz, vp]
+        lib.dash_pages_reserve.argtypes = [G, vp, i, vp, vp, sz, vp]
+        lib.dash_pages_fork.argtypes = [G, vp, vp, i, vp, vp, sz, vp]
+        lib.dash_pages_free.argtypes = [G, vp, i, vp, vp]
+        lib.dash_pages_compact.argtypes = [G, vp, vp, sz, vp]
+        for name in ("append_q4", "load_q4", "decode_q4", "pages_copy", "pages_reserve", "pages_fork", "pages_free",
+                     "pages_compact"):
+            getattr(lib, "dash_" + name).restype = ctypes.c_int
         lib.dash_status_string.argtypes = [ctypes.c_int]
         lib.dash_status_string.restype = ctypes.c_char_p
         lib.dash_set_wait_limit.argtypes = [ctypes.c_longlong]
@@ -92,9 +134,9 @@ def load():
     return _lib
 
 
-def header_symbols():
-    """Entry points declared in include/dash.h."""
-    with open(HEADER) as fh:
+def header_symbols(header=HEADER):
+    """Entry points declared in include/dash.h (or another header of the library)."""
+    with open(header) as fh:
         text = fh.read()
     return sorted(set(re.findall(r"^\s*(?:size_t|int|long long|const char\*)\s+(dash_\w+)\s*\(", text, re.M)))
 
@@ -249,4 +291,82 @@ def dash_backward(p, Q, K, V, qbar, dO, kbar, route, dQ, dK, dV, dqbar, workspac
                               ctypes.byref(route) if route is not None else None, _ptr(dQ), _ptr(dK), _ptr(dV),
                               _ptr(dqbar), _ptr(workspace), ws_bytes, _stream(stream))
     _check(rc, "dash_backward")
+    return rc
+
+
+# ---- include/dash_cache.h: 4-bit caches and pages -----------------------------------------------------
+def q4_kv(k_codes, k_scales, v_codes, v_scales, page_table, *, page_size, k_exp=0, v_exp=0):
+    """Description of 4-bit pools: uint8 codes [num_pages, h_kv, page_size, d / 2] and scales
+    [num_pages, h_kv, page_size, d / 32], device int32 page_table [batch, max_pages]."""
+    return dash_q4_kv(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), k_codes.stride(0),
+                      k_scales.stride(0), v_codes.stride(0), v_scales.stride(0), _ptr(page_table),
+                      int(page_table.shape[1]), int(page_size), int(k_codes.shape[0]), int(k_exp), int(v_exp))
+
+
+def dash_q4_workspace_size(p: dash_params) -> int:
+    return int(load().dash_q4_workspace_size(ctypes.byref(p)))
+
+
+def dash_append_q4(p, kv, k_new, v_new, n_new, counts, qbar, kbar_cache, partial_state, seqlens, stream=None) -> int:
+    rc = load().dash_append_q4(p, kv, _ptr(k_new), _ptr(v_new), int(n_new), _ptr(counts), _ptr(qbar),
+                               _ptr(kbar_cache), _ptr(partial_state), _ptr(seqlens), _stream(stream))
+    _check(rc, "dash_append_q4")
+    return rc
+
+
+def dash_load_q4(p, kv, start, offset, n, seqlens, K, V, stream=None) -> int:
+    rc = load().dash_load_q4(p, kv, _ptr(start), int(offset), int(n), _ptr(seqlens), _ptr(K), _ptr(V),
+                             _stream(stream))
+    _check(rc, "dash_load_q4")
+    return rc
+
+
+def dash_decode_q4(p, kv, q, kbar_cache, seqlens, O, route=None, workspace=None, ws_bytes=None, stream=None) -> int:
+    if ws_bytes is None:
+        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    rc = load().dash_decode_q4(p, kv, _ptr(q), _ptr(kbar_cache), _ptr(seqlens), _ptr(O), route, _ptr(workspace),
+                               ws_bytes, _stream(stream))
+    _check(rc, "dash_decode_q4")
+    return rc
+
+
+def pages(page_table, refs, seqlens, *, page_size, arrays=(), rows=()):
+    """dash_pages over device int32 page_table [batch, max_pages], refs [num_pages], seqlens [batch];
+    arrays / rows are dash_page_array / dash_row_array."""
+    a, r = (dash_page_array * len(arrays))(*arrays), (dash_row_array * len(rows))(*rows)
+    return dash_pages(int(page_table.shape[0]), int(page_table.shape[1]), int(page_size), int(refs.shape[0]),
+                      _ptr(page_table), _ptr(refs), _ptr(seqlens), a, r, len(arrays), len(rows))
+
+
+def dash_pages_workspace_size(pg: dash_pages) -> int:
+    return int(load().dash_pages_workspace_size(pg))
+
+
+def dash_pages_copy(pg, src, dst, n, status, workspace, ws_bytes, stream=None) -> int:
+    rc = load().dash_pages_copy(pg, _ptr(src), _ptr(dst), n, _ptr(status), _ptr(workspace), ws_bytes, _stream(stream))
+    _check(rc, "dash_pages_copy")
+    return rc
+
+
+def dash_pages_reserve(pg, counts, count, status, workspace, ws_bytes, stream=None) -> int:
+    rc = load().dash_pages_reserve(pg, _ptr(counts), count, _ptr(status), _ptr(workspace), ws_bytes, _stream(stream))
+    _check(rc, "dash_pages_reserve")
+    return rc
+
+
+def dash_pages_fork(pg, src, dst, n, status, workspace, ws_bytes, stream=None) -> int:
+    rc = load().dash_pages_fork(pg, _ptr(src), _ptr(dst), n, _ptr(status), _ptr(workspace), ws_bytes, _stream(stream))
+    _check(rc, "dash_pages_fork")
+    return rc
+
+
+def dash_pages_free(pg, rows, n, status, stream=None) -> int:
+    rc = load().dash_pages_free(pg, _ptr(rows), n, _ptr(status), _stream(stream))
+    _check(rc, "dash_pages_free")
+    return rc
+
+
+def dash_pages_compact(pg, used, workspace, ws_bytes, stream=None) -> int:
+    rc = load().dash_pages_compact(pg, _ptr(used), _ptr(workspace), ws_bytes, _stream(stream))
+    _check(rc, "dash_pages_compact")
     return rc

@@ -1,0 +1,547 @@
+// pages.cu -- operations on the pages of a cache (include/dash_cache.h): copy, reserve, fork, free,
+// compact.
+//
+// Each operation that moves data is two launches.  A plan (one block: the lists are short and the
+// results must not depend on timing) checks the request, picks pages in ascending order with block
+// scans over the reference counts, and leaves a list of (source, destination) pages in the
+// workspace; the mover spreads the list's bytes over the whole GPU.  A request that fails its
+// checks leaves an empty list, so nothing changes.  The mover is bound by HBM (2 bytes moved per
+// byte of a page); small requests by the two launches, which overlap (programmatic dependent
+// launch).
+#include "q4.cuh"
+#include "pages.cuh"
+
+namespace dash {
+namespace {
+
+constexpr int kPlan = 1024;             // threads of a plan block
+constexpr int kMove = 256;              // threads of a mover block
+constexpr long long kSeg = 8192;        // bytes a mover block takes at a time: two 16-byte loads per thread in flight
+constexpr int kSlots = 1024;            // table entries it takes at a time
+
+// Workspace header, then the lists (see PagesWs).
+struct Plan {
+    int pairs;      // pages to copy
+    int ok;         // the request passed its checks (rows and tables may change)
+    int used;       // compaction: pages in use
+    int pad;
+};
+
+__device__ __forceinline__ void fail(int* status, int code)
+{
+    if (status) atomicCAS(status, 0, code);
+}
+
+// The lowest failure code that any thread of the plan block has in its mask (bit = code), stored;
+// 0 if there is none.  Called by the whole block.
+__device__ int first_failure(unsigned mask, int* status)
+{
+    __shared__ unsigned all;
+    if (threadIdx.x == 0) all = 0;
+    __syncthreads();
+    if (mask) atomicOr(&all, mask);
+    __syncthreads();
+    const int code = all ? __ffs(all) - 1 : 0;
+    if (code && threadIdx.x == 0) fail(status, code);
+    __syncthreads();
+    return code;
+}
+
+// Exclusive prefix of v over the block's threads in order; *total = the block's sum.
+__device__ int block_scan(int v, int* total)
+{
+    __shared__ int ws[kPlan / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += u;
+    }
+    if (lane == 31) ws[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int y = ws[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) y += u;
+        }
+        ws[lane] = y;
+    }
+    __syncthreads();
+    const int before = warp ? ws[warp - 1] : 0;
+    *total = ws[kPlan / 32 - 1];
+    __syncthreads();
+    return before + x - v;
+}
+
+constexpr int kPer = 8;   // pages a thread looks at per step
+
+// The `want` lowest pages with refs == 0, ascending, into list; returns how many there are (at most
+// want).  Called by the whole plan block.
+__device__ int lowest_free(const int* refs, int pages, int want, int* list)
+{
+    int found = 0;
+    for (int p0 = 0; p0 < pages && found < want; p0 += kPlan * kPer) {
+        const int p = p0 + threadIdx.x * kPer;
+        unsigned m = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+            if (p + k < pages && refs[p + k] == 0) m |= 1u << k;
+        int total;
+        int at = found + block_scan(__popc(m), &total);
+        for (; m; m &= m - 1, ++at)
+            if (at < want) list[at] = p + __ffs(m) - 1;
+        found += total;
+    }
+    __syncthreads();
+    return min(found, want);
+}
+
+// ---- plans ------------------------------------------------------------------------------------------
+// copy: destinations distinct and not sources.  mark[page] = the entry that writes it; a stale or
+// foreign mark is recognised by looking the entry up, so the marks need no clearing.
+__global__ void __launch_bounds__(kPlan) plan_copy_kernel(PageTab t, const int* src, const int* dst, int n, int* status,
+                                                          PagesWs w)
+{
+    pdl_launch_dependents();
+    Plan* plan = reinterpret_cast<Plan*>(w.head);
+    unsigned bad = 0;
+    for (int i = threadIdx.x; i < n; i += kPlan) {
+        const int s = src[i], d = dst[i];
+        if (s < 0 || s >= t.num_pages || d < 0 || d >= t.num_pages) bad |= 1u << DASH_PAGES_INDEX;
+        else w.mark[d] = i;
+    }
+    int code = first_failure(bad, status);
+    if (!code) {
+        for (int i = threadIdx.x; i < n; i += kPlan) {
+            const int s = src[i], d = dst[i], k = w.mark[s];
+            if (w.mark[d] != i) bad |= 1u << DASH_PAGES_TWICE;
+            // a page that some entry writes is read: only fine where that entry copies it onto itself
+            if (k >= 0 && k < n && dst[k] == s && src[k] != s) bad |= 1u << DASH_PAGES_TWICE;
+            w.src[i] = s;
+            w.dst[i] = d;
+        }
+        code = first_failure(bad, status);
+    }
+    if (threadIdx.x == 0) { plan->pairs = code ? 0 : n; plan->ok = !code; }
+}
+
+// reserve: a warp per row counts the slots it lacks; then, if there are enough free pages, fills them.
+__global__ void __launch_bounds__(kPlan) reserve_kernel(PageTab t, const int* counts, int count, int* status, PagesWs w)
+{
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned bad = 0;
+    auto slots = [&](int b, int* s0, int* s1) {
+        const int L = t.seqlens[b], add = counts ? counts[b] : count;
+        *s0 = *s1 = 0;
+        if (add <= 0) return;
+        const long long end = (long long)L + add;
+        if (L < 0 || end > (long long)t.max_pages * t.page_size) { bad |= 1u << DASH_PAGES_LENGTH; return; }
+        *s0 = L / t.page_size;
+        *s1 = (int)((end + t.page_size - 1) / t.page_size);
+    };
+    for (int b = warp; b < t.batch; b += kPlan / 32) {
+        int s0, s1, n = 0;
+        slots(b, &s0, &s1);
+        for (int k = s0; k < s1; k += 32)
+            n += __popc(__ballot_sync(0xffffffffu, k + lane < s1 && t.page_table[(long long)b * t.max_pages + k + lane] < 0));
+        if (lane == 0) w.row[b] = n;
+    }
+    if (first_failure(bad, status)) return;
+    int want = 0;
+    for (int b0 = 0; b0 < t.batch; b0 += kPlan) {
+        const int b = b0 + threadIdx.x, n = b < t.batch ? w.row[b] : 0;
+        int total;
+        const int at = block_scan(n, &total);
+        if (b < t.batch) w.row[b] = want + at;   // pages given to the rows before
+        want += total;
+    }
+    __syncthreads();
+    if (want == 0) return;
+    if (want > t.num_pages || lowest_free(t.refs, t.num_pages, want, w.dst) < want) {
+        if (threadIdx.x == 0) fail(status, DASH_PAGES_FULL);
+        return;
+    }
+    for (int b = warp; b < t.batch; b += kPlan / 32) {
+        int s0, s1, at = w.row[b];
+        slots(b, &s0, &s1);
+        for (int k = s0; k < s1; k += 32) {
+            int* e = t.page_table + (long long)b * t.max_pages + k + lane;
+            const bool on = k + lane < s1 && *e < 0;
+            const unsigned m = __ballot_sync(0xffffffffu, on);
+            if (on) {
+                const int pg = w.dst[at + __popc(m & ((1u << lane) - 1u))];
+                *e = pg;
+                t.refs[pg] = 1;
+            }
+            at += __popc(m);
+        }
+    }
+}
+
+// fork: checks, a page for every child whose parent ends inside one.  Leaves the parent's length
+// (w.row) and the child's own page (w.own, -1) per entry: the mover writes tables and lengths.
+__global__ void __launch_bounds__(kPlan) plan_fork_kernel(PageTab t, const int* src, const int* dst, int n, int* status,
+                                                          PagesWs w)
+{
+    pdl_launch_dependents();
+    Plan* plan = reinterpret_cast<Plan*>(w.head);
+    unsigned bad = 0;
+    for (int i = threadIdx.x; i < n; i += kPlan) {
+        const int s = src[i], d = dst[i];
+        if (s < 0 || s >= t.batch || d < 0 || d >= t.batch) { bad |= 1u << DASH_PAGES_INDEX; continue; }
+        w.mark[d] = i;
+        const int L = t.seqlens[s];
+        if (L < 0 || L > (long long)t.max_pages * t.page_size) { bad |= 1u << DASH_PAGES_LENGTH; continue; }
+        if (t.seqlens[d] != 0 || t.page_table[(long long)d * t.max_pages] >= 0) bad |= 1u << DASH_PAGES_BUSY;
+        w.row[i] = L;
+    }
+    int code = first_failure(bad, status), want = 0;
+    if (!code) {
+        for (int i0 = 0; i0 < n; i0 += kPlan) {
+            const int i = i0 + threadIdx.x;
+            int part = 0, pg = -1;
+            if (i < n) {
+                const int k = w.mark[src[i]];
+                if (w.mark[dst[i]] != i || (k >= 0 && k < n && dst[k] == src[i])) bad |= 1u << DASH_PAGES_TWICE;
+                const int L = w.row[i];
+                part = L % t.page_size != 0;
+                if (part) {
+                    pg = t.page_table[(long long)src[i] * t.max_pages + L / t.page_size];
+                    if (pg < 0 || pg >= t.num_pages) bad |= 1u << DASH_PAGES_INDEX;
+                }
+            }
+            int total;
+            const int at = want + block_scan(part, &total);
+            if (i < n) w.own[i] = part ? at : -1;
+            if (part) w.src[at] = pg;
+            want += total;
+        }
+        code = first_failure(bad, status);
+    }
+    if (!code && want && (want > t.num_pages || lowest_free(t.refs, t.num_pages, want, w.dst) < want))
+        code = first_failure(1u << DASH_PAGES_FULL, status);
+    if (!code)
+        for (int i = threadIdx.x; i < n; i += kPlan)
+            if (w.own[i] >= 0) {
+                w.own[i] = w.dst[w.own[i]];
+                t.refs[w.own[i]] = 1;
+            }
+    if (threadIdx.x == 0) { plan->pairs = code ? 0 : want; plan->ok = !code; }
+}
+
+// compact: U = pages in use; the k-th free page below U receives the k-th used page from U on.
+__global__ void __launch_bounds__(kPlan) plan_compact_kernel(PageTab t, int* used, PagesWs w)
+{
+    pdl_launch_dependents();
+    Plan* plan = reinterpret_cast<Plan*>(w.head);
+    int U = 0;
+    for (int p = threadIdx.x; p < t.num_pages; p += kPlan) U += t.refs[p] > 0;
+    {
+        int total;
+        block_scan(U, &total);
+        U = total;
+    }
+    int holes = 0, movers = 0;
+    for (int p0 = 0; p0 < t.num_pages; p0 += kPlan * kPer) {
+        const int p = p0 + threadIdx.x * kPer;
+        unsigned h = 0, m = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            if (p + k >= t.num_pages) continue;
+            const bool on = t.refs[p + k] > 0;
+            if (p + k < U && !on) h |= 1u << k;
+            if (p + k >= U && on) m |= 1u << k;
+            if (p + k >= U && !on) w.mark[p + k] = p + k;   // table entries of pages without a count stay
+        }
+        int total;   // both counts in one scan: at most 8192 of each per step
+        const int at = block_scan(__popc(h) | __popc(m) << 16, &total);
+        int a = holes + (at & 0xffff), c = movers + (at >> 16);
+        for (; h; h &= h - 1) w.dst[a++] = p + __ffs(h) - 1;
+        for (; m; m &= m - 1) w.src[c++] = p + __ffs(m) - 1;
+        holes += total & 0xffff;
+        movers += total >> 16;
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < movers; k += kPlan) {
+        const int s = w.src[k], d = w.dst[k];
+        w.mark[s] = d;
+        t.refs[d] = t.refs[s];
+        t.refs[s] = 0;
+    }
+    if (threadIdx.x == 0) {
+        plan->pairs = movers;
+        plan->ok = 1;
+        plan->used = U;
+        if (used) *used = U;
+    }
+}
+
+// ---- mover --------------------------------------------------------------------------------------------
+// Work of one launch, taken unit by unit: first the listed pages of up to kArrays arrays (pieces of
+// kSeg bytes), then, for a fork, the rows of up to kArrays row arrays, then the tables.
+enum { MOVE_PAGES = 0, MOVE_FORK = 1, MOVE_COMPACT = 2 };
+
+struct Move {
+    MoveArray pages[kArrays];
+    MoveRows rows[kArrays];
+    int np, nr, segs;               // arrays, row arrays, pieces per page over all arrays
+    long long row_units;            // pieces per forked row over all row arrays
+    int op, n;                      // fork: entries
+    const int *src, *dst;           // fork: the row lists
+    int tables;                     // this launch writes the tables
+};
+
+__device__ __forceinline__ void copy_bytes(char* dst, const char* src, long long bytes, bool wide)
+{
+    if (wide) {
+        const int n = (int)(bytes >> 4);
+        const uint4* s = reinterpret_cast<const uint4*>(src);
+        uint4* d = reinterpret_cast<uint4*>(dst);
+        const int i = threadIdx.x, j = i + kMove;
+        uint4 u, v;
+        if (i < n) u = __ldcs(s + i);
+        if (j < n) v = __ldcs(s + j);
+        if (i < n) __stcs(d + i, u);
+        if (j < n) __stcs(d + j, v);
+    } else {
+        const int n = (int)(bytes >> 2);
+        for (int i = threadIdx.x; i < n; i += kMove)
+            reinterpret_cast<uint32_t*>(dst)[i] = reinterpret_cast<const uint32_t*>(src)[i];
+    }
+}
+static_assert(kSeg == 2 * 16 * kMove, "a piece is two vectors per thread");
+
+__global__ void __launch_bounds__(kMove) move_kernel(PageTab t, PagesWs w, const __grid_constant__ Move mv)
+{
+    pdl_wait();   // the plan
+    pdl_launch_dependents();
+    const Plan* plan = reinterpret_cast<const Plan*>(w.head);
+    if (!plan->ok) return;
+    const long long page_units = (long long)plan->pairs * mv.segs;
+    const long long row_units = mv.op == MOVE_FORK ? mv.row_units * mv.n : 0;
+    const int per_row = (t.max_pages + kSlots - 1) / kSlots;
+    const long long tab_rows = !mv.tables ? 0 : mv.op == MOVE_FORK ? mv.n : t.batch;
+    const long long total = page_units + row_units + tab_rows * per_row;
+    for (long long u = blockIdx.x; u < total; u += gridDim.x) {
+        if (u < page_units) {
+            const int k = (int)(u / mv.segs);
+            int q = (int)(u % mv.segs), a = 0;
+            while (q >= mv.pages[a].segs) q -= mv.pages[a++].segs;
+            const MoveArray& m = mv.pages[a];
+            const long long off = q * kSeg;
+            copy_bytes(m.data + (long long)w.dst[k] * m.stride + off, m.data + (long long)w.src[k] * m.stride + off,
+                       min(kSeg, m.bytes - off), true);
+        } else if (u < page_units + row_units) {
+            const long long v = u - page_units;
+            const int k = (int)(v / mv.row_units);
+            long long q = v % mv.row_units;
+            int a = 0;
+            while (q >= (long long)mv.rows[a].heads * mv.rows[a].segs) {
+                q -= (long long)mv.rows[a].heads * mv.rows[a].segs;
+                ++a;
+            }
+            const MoveRows& m = mv.rows[a];
+            const int h = (int)(q / m.segs);
+            const long long off = q % m.segs * kSeg;
+            const int in_use = m.unit_tokens > 0 ? min(m.max_units, w.row[k] / m.unit_tokens) : m.max_units;
+            const long long left = in_use * m.unit_bytes - off;
+            if (left > 0) {
+                const long long at = h * m.head_stride + off;
+                copy_bytes(m.data + mv.dst[k] * m.row_stride + at, m.data + mv.src[k] * m.row_stride + at,
+                           min(kSeg, left), m.wide);
+            }
+        } else {
+            const long long v = u - page_units - row_units;
+            const int k = (int)(v / per_row), s0 = (int)(v % per_row) * kSlots, s1 = min(t.max_pages, s0 + kSlots);
+            if (mv.op == MOVE_FORK) {
+                const int L = w.row[k], full = L / t.page_size, own = w.own[k];
+                const int* from = t.page_table + (long long)mv.src[k] * t.max_pages;
+                int* to = t.page_table + (long long)mv.dst[k] * t.max_pages;
+                for (int s = s0 + threadIdx.x; s < s1; s += kMove) {
+                    int e = -1;
+                    if (s < full) {
+                        e = from[s];
+                        if (e >= 0 && e < t.num_pages) atomicAdd(t.refs + e, 1);
+                    } else if (s == full) {
+                        e = own;
+                    }
+                    to[s] = e;
+                }
+                if (s0 == 0 && threadIdx.x == 0) t.seqlens[mv.dst[k]] = L;
+            } else {
+                for (int s = s0 + threadIdx.x; s < s1; s += kMove) {
+                    int* e = t.page_table + (long long)k * t.max_pages + s;
+                    const int p = *e;
+                    if (p >= plan->used && p < t.num_pages) *e = w.mark[p];
+                }
+            }
+        }
+    }
+}
+
+// free: one block per (entry, part of its row); of equal entries the first acts.
+struct Clear {
+    MoveRows rows[kArrays];
+    int n, tables;
+};
+__global__ void __launch_bounds__(kMove) free_kernel(PageTab t, const int* rows, int n, int* status,
+                                                     const __grid_constant__ Clear c)
+{
+    const int i = blockIdx.x, b = rows[i];
+    if (b < 0 || b >= t.batch) {
+        if (threadIdx.x == 0) fail(status, DASH_PAGES_INDEX);
+        return;
+    }
+    bool again = false;
+    for (int j = threadIdx.x; j < i; j += kMove) again = again || rows[j] == b;
+    if (__syncthreads_or(again)) return;
+    const int s0 = blockIdx.y * kSlots, s1 = min(t.max_pages, s0 + kSlots);
+    if (s0 == 0)
+        for (int a = 0; a < c.n; ++a) {
+            const MoveRows& m = c.rows[a];
+            const long long words = m.max_units * m.unit_bytes / 4;
+            for (int h = 0; h < m.heads; ++h)
+                for (long long k = threadIdx.x; k < words; k += kMove)
+                    reinterpret_cast<int*>(m.data + b * m.row_stride + h * m.head_stride)[k] = 0;
+        }
+    if (!c.tables) return;
+    for (int s = s0 + threadIdx.x; s < s1; s += kMove) {
+        int* e = t.page_table + (long long)b * t.max_pages + s;
+        const int p = *e;
+        *e = -1;
+        if (p >= 0 && p < t.num_pages) atomicSub(t.refs + p, 1);
+    }
+    if (s0 == 0 && threadIdx.x == 0) t.seqlens[b] = 0;
+}
+
+MoveRows rows_of(const dash_row_array& p)
+{
+    MoveRows m;
+    m.data = (char*)p.data;
+    m.row_stride = p.row_stride;
+    m.head_stride = p.head_stride;
+    m.unit_bytes = p.unit_bytes;
+    m.heads = p.heads;
+    m.max_units = p.max_units;
+    m.unit_tokens = p.unit_tokens;
+    m.segs = (int)((p.max_units * p.unit_bytes + kSeg - 1) / kSeg);
+    m.wide = (reinterpret_cast<uintptr_t>(p.data) | (uintptr_t)p.row_stride | (uintptr_t)p.head_stride |
+              (uintptr_t)p.unit_bytes) % 16 == 0;
+    return m;
+}
+
+// Enough blocks for 8 per SM, or one per unit of a small request.
+dim3 move_grid(long long units)
+{
+    const long long most = 8ll * dec_tma_blocks();
+    return dim3((unsigned)(units < 1 ? 1 : units < most ? units : most));
+}
+
+// The mover's launches: the arrays in groups of kArrays.
+cudaError_t launch_move(const PageTab& t, const PagesWs& w, const dash_pages* pg, int op, int n, const int* src,
+                        const int* dst, long long most_pairs, cudaStream_t st)
+{
+    int a = 0, r = 0;
+    bool first = true;
+    const int nr = op == MOVE_FORK ? pg->num_rows : 0;
+    while (first || a < pg->num_arrays || r < nr) {
+        Move mv = {};
+        mv.op = op;
+        mv.n = n;
+        mv.src = src;
+        mv.dst = dst;
+        mv.tables = first && op != MOVE_PAGES;
+        for (; a < pg->num_arrays && mv.np < kArrays; ++a) {
+            const dash_page_array& p = pg->arrays[a];
+            if (p.page_bytes == 0) continue;
+            MoveArray& m = mv.pages[mv.np++];
+            m.data = (char*)p.data;
+            m.bytes = p.page_bytes;
+            m.stride = p.page_stride;
+            m.segs = (int)((p.page_bytes + kSeg - 1) / kSeg);
+            mv.segs += m.segs;
+        }
+        for (; r < nr && mv.nr < kArrays; ++r) {
+            const dash_row_array& p = pg->rows[r];
+            if (p.unit_bytes == 0 || p.heads == 0 || p.max_units == 0) continue;
+            const MoveRows& m = mv.rows[mv.nr++] = rows_of(p);
+            mv.row_units += (long long)m.heads * m.segs;
+        }
+        const long long tab = mv.tables ? (long long)(op == MOVE_FORK ? n : t.batch) * ((t.max_pages + kSlots - 1) / kSlots) : 0;
+        const cudaError_t e = launch_after(move_kernel, move_grid(most_pairs * mv.segs + mv.row_units * n + tab),
+                                           dim3(kMove), 0, st, t, w, mv);
+        if (e != cudaSuccess) return e;
+        first = false;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+size_t pages_ws(const PageTab& t, char* base, PagesWs* w)
+{
+    size_t at = 256;
+    auto take = [&](size_t ints) {
+        int* p = reinterpret_cast<int*>(base + at);
+        at += (ints * 4 + 255) / 256 * 256;
+        return p;
+    };
+    const size_t big = t.num_pages > t.batch ? t.num_pages : t.batch;
+    w->head = base;
+    w->src = take(big);
+    w->dst = take(big);
+    w->mark = take(big);
+    w->row = take(t.batch);
+    w->own = take(t.batch);
+    return at;
+}
+
+cudaError_t launch_pages_copy(const PageTab& t, const dash_pages* pg, const int* src, const int* dst, int n, int* status,
+                              const PagesWs& w, cudaStream_t st)
+{
+    plan_copy_kernel<<<1, kPlan, 0, st>>>(t, src, dst, n, status, w);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_move(t, w, pg, MOVE_PAGES, 0, nullptr, nullptr, n, st);
+}
+
+cudaError_t launch_pages_reserve(const PageTab& t, const int* counts, int count, int* status, const PagesWs& w,
+                                 cudaStream_t st)
+{
+    reserve_kernel<<<1, kPlan, 0, st>>>(t, counts, count, status, w);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_pages_fork(const PageTab& t, const dash_pages* pg, const int* src, const int* dst, int n, int* status,
+                              const PagesWs& w, cudaStream_t st)
+{
+    plan_fork_kernel<<<1, kPlan, 0, st>>>(t, src, dst, n, status, w);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_move(t, w, pg, MOVE_FORK, n, src, dst, n, st);
+}
+
+cudaError_t launch_pages_free(const PageTab& t, const dash_pages* pg, const int* rows, int n, int* status, cudaStream_t st)
+{
+    int r = 0;
+    for (bool first = true; first || r < pg->num_rows; first = false) {
+        Clear c = {};
+        c.tables = first;
+        for (; r < pg->num_rows && c.n < kArrays; ++r)
+            if (pg->rows[r].clear) c.rows[c.n++] = rows_of(pg->rows[r]);
+        if (!first && c.n == 0) break;
+        free_kernel<<<dim3(n, first ? (t.max_pages + kSlots - 1) / kSlots : 1), kMove, 0, st>>>(t, rows, n, status, c);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_pages_compact(const PageTab& t, const dash_pages* pg, int* used, const PagesWs& w, cudaStream_t st)
+{
+    plan_compact_kernel<<<1, kPlan, 0, st>>>(t, used, w);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_move(t, w, pg, MOVE_COMPACT, 0, nullptr, nullptr, t.num_pages / 2, st);
+}
+
+}  // namespace dash

@@ -1,0 +1,569 @@
+// q4_decode.cu -- decode attention over a K/V cache held in 4 bits (format: include/dash_cache.h).
+//
+// One query per sequence, g heads of a KV head share the keys (Proposition 4.1):
+//   o = sum_j 2^(z_j) v_j / sum_j 2^(z_j),  z_j = <q, k_j> log2(e)/sqrt(d) + bias_j log2(e)
+// over the routed chunks (bias of the chunk) and the query's own chunk (bias 0); gamma = 0 takes
+// every chunk with bias 0.
+//
+// Work is cut into granules of 16 tokens.  The granules of all (sequence, KV head) pairs form one
+// list that the blocks share evenly; a block's warps take its granules in turn, each with its own
+// online softmax and its own ring of cp.async stages (a granule is used by one warp only, so no
+// barrier is involved), and merge at the end of a pair.  A pair inside one block is finished there;
+// pieces of a pair that spans blocks are merged by a second kernel, in block order.
+//
+// A warp computes S^T = K q^T and O^T = V^T P^T: the 16 tokens (then 16 of the d_h elements) are the
+// 16 rows of m16n8k16 MMAs and the heads the 8 columns, so groups of up to 8 heads fill the tile.
+//   K: the operand is 128 + u (bf16, one mask-or per two codes), straight from a 16-byte load: key
+//      rows are stored in the order of the operand's registers.  The accumulator starts at
+//      -136 sum(q) over the scale group, which takes the offset off, and each group's sum is
+//      multiplied by the key's scale in fp32: the codes enter the product exactly.
+//   V: the operand needs the scale inside the sum over tokens.  1024 + u (or 1024 + 16 u) in f16,
+//      one f16x2 fma (1024 + u) s' - 1032 s' gives (u - 8) s' exactly: with s' = scale / 16,
+//      1032 s' has at most 8 + 4 - 1 = 11 significant bits (129 * 15 < 2^11) and is below 2^15.
+//   P is rounded to f16 (2^-12 relative; sums of P are taken before the rounding, in fp32) and
+//   turned from S^T's accumulator layout into an operand by movmatrix.
+// The reference of the softmax moves only when a logit exceeds it by more than 6 (P <= 64 in f16).
+//
+// Bound: HBM, 2 x 17/32 bytes per (key element, value element); close behind it the integer and
+// f16 pipes that unpack the codes.
+#include <cuda_fp16.h>
+
+#include "q4.cuh"
+#include "stage2_mma.cuh"
+
+namespace dash {
+namespace {
+
+constexpr int kGran = 16;         // tokens per granule
+constexpr int kStages = 4;
+constexpr int kMaxPairs = 2048;
+constexpr int kMeta = 64;         // granule descriptors per warp (two halves of 32)
+
+// Warps per block: one block per SM, as many warps as the registers of NT head tiles allow.
+template <int NT> struct Cfg { static constexpr int W = NT == 1 ? 16 : 12; };
+
+template <int D>
+struct Stage {
+    static constexpr int CODES = kGran * D / 2, SCALES = kGran * D / kGrp;
+    static constexpr int K = 0, V = CODES, KS = 2 * CODES, VS = 2 * CODES + SCALES, BYTES = 2 * (CODES + SCALES);
+    static constexpr int OLD = D + 4;   // row length of the merge buffer [8 NT][OLD] that reuses a warp's ring
+};
+
+struct Attend {
+    const __nv_bfloat16* q;
+    const int* seqlens;
+    int dense;        // every chunk before the query's own, bias 0 (no route lists)
+    float* part;      // [block][first, last][g][D + 2]: partial o, reference, sum
+    int* pre;         // [pairs + 2]: granules before each pair, total, blocks in use
+    __nv_bfloat16* O;
+};
+
+__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+                 "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movm_t(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t h2(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
+__device__ __forceinline__ __half2 h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
+
+// 128 + code i and 128 + code i + 4 of a word, as bf16x2
+__device__ __forceinline__ uint32_t k_pair(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u; }
+
+// Token (row of the granule) behind row m < 8 of S^T (row m + 8: the same + 8).  Even rows 0..3 and
+// odd rows 5, 4, 7, 6: keys read two rows of opposite parity at once, values rows 0..3 or 4..7,
+// which the swizzle of the value rows spreads over all banks.
+__device__ __forceinline__ int tok_of(int m) { return (m & 1) ? ((m >> 1) ^ 1) + 4 : m >> 1; }
+
+// Length of sequence b as the kernels use it, granules of a pair.
+__device__ __forceinline__ int len_of(const Shape& s, const int* seqlens, int b) { return min(max(seqlens[b], 0), s.n); }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, Q4 c, Routes rt, Attend a)
+{
+    constexpr int W = Cfg<NT>::W, NG = D / kGrp, NW = D / 64, MT = D / 16, OLD = Stage<D>::OLD;
+    using St = Stage<D>;
+    static_assert(8 * NT * OLD * 4 <= kStages * St::BYTES, "the merge buffer reuses a warp's ring");
+    extern __shared__ __align__(128) char smem[];
+    __shared__ int pre[kMaxPairs + 1];
+    __shared__ float mrg_m[W][8 * NT], mrg_l[W][8 * NT], mrg_s[W][8 * NT], tot_m[8 * NT], tot_l[8 * NT];
+    __shared__ int meta_pg[W][kMeta], meta_at[W][kMeta];
+    __shared__ float meta_b[W][kMeta];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const int BR = s.batch * s.hkv, G = s.g, NB = s.B / kGran;
+    pdl_wait();   // the routes and the appended tokens of this step
+    pdl_launch_dependents();
+    for (int x = threadIdx.x; x < BR; x += 32 * W) {
+        const int L = len_of(s, a.seqlens, x / s.hkv);
+        const int full = L > 0 ? (a.dense ? (L - 1) / s.B : rt.counts[x]) : 0;
+        pre[x + 1] = L > 0 ? full * NB + ((L - 1) % s.B) / kGran + 1 : 0;
+    }
+    if (threadIdx.x == 0) pre[0] = 0;
+    __syncthreads();
+    if (warp == 0) {
+        int run = 0;
+        for (int x0 = 0; x0 < BR; x0 += 32) {
+            int v = x0 + lane < BR ? pre[x0 + lane + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            if (x0 + lane < BR) pre[x0 + lane + 1] = run + v;
+            run += __shfl_sync(0xffffffffu, v, 31);
+        }
+    }
+    __syncthreads();
+    const long long total = pre[BR];
+    // every warp of a block in use has a granule
+    const int used = (int)min((long long)gridDim.x, (total + W - 1) / W);
+    if (blockIdx.x == 0) {
+        for (int x = threadIdx.x; x <= BR; x += 32 * W) a.pre[x] = pre[x];
+        if (threadIdx.x == 0) a.pre[BR + 1] = used;
+    }
+    if ((int)blockIdx.x >= used) return;
+    const int lo = (int)(total * blockIdx.x / used), hi = (int)(total * (blockIdx.x + 1) / used);
+
+    char* ring = smem + warp * (kStages * St::BYTES);
+    const uint32_t ring_a = smem_u32(ring);
+    const float scale2 = kLog2e * rsqrtf((float)D) * exp2i(c.kexp);
+    const float out_scale = 16.f * exp2i(c.vexp);
+    const int tk = tok_of(g);                        // this lane's key rows: tk, tk + 8
+    const int vr0 = t4, vr1 = (t4 ^ 1) + 4;          // its value rows: vr0, vr1, vr0 + 8, vr1 + 8
+
+    int x = 0;
+    {   // first pair with granules in this block's range
+        int l = 0, h = BR;
+        while (l < h) {
+            const int m = (l + h) >> 1;
+            if (pre[m + 1] <= lo) l = m + 1;
+            else h = m;
+        }
+        x = l;
+    }
+    for (; x < BR && pre[x] < hi; ++x) {
+        const int p0 = pre[x], p1 = pre[x + 1];
+        const int s_lo = max(lo, p0), s_hi = min(hi, p1);
+        if (s_lo >= s_hi) continue;
+        const int b = x / s.hkv, r = x % s.hkv, i = len_of(s, a.seqlens, b) - 1;
+        const int full = p1 - p0 - ((i % s.B) / kGran + 1);   // granules of routed chunks
+        const int nm = max(0, (s_hi - s_lo - warp + W - 1) / W);
+
+        // ---- granule descriptors, 32 at a time (page, row and number of tokens, bias) ----------------
+        int f_pg = -1, f_at = 0;
+        float f_b = 0.f;
+        auto fetch = [&](int m0) {
+            const int m = m0 + lane;
+            if (m >= nm) return;
+            const int t = s_lo - p0 + warp + m * W;
+            int tok, nv = kGran;
+            f_b = 0.f;
+            if (t < full) {
+                int ch = t / NB;
+                if (!a.dense) {
+                    f_b = rt.bias[(long long)x * rt.cap + ch] * kLog2e;
+                    ch = rt.idx[(long long)x * rt.cap + ch];
+                }
+                tok = ch * s.B + (t % NB) * kGran;
+            } else {
+                tok = (i / s.B) * s.B + (t - full) * kGran;
+                nv = min(kGran, i + 1 - tok);
+            }
+            f_pg = q4_page(c, b, tok);
+            f_at = tok % c.psz | (nv - 1);   // rows of granules are multiples of 16
+        };
+        auto publish = [&](int m0) {
+            const int k = (m0 & 32) + lane;
+            meta_pg[warp][k] = f_pg;
+            meta_at[warp][k] = f_at;
+            meta_b[warp][k] = f_b;
+            __syncwarp();
+        };
+        auto issue = [&](int m) {
+            if (m < nm) {
+                const int pg = meta_pg[warp][m & 63];
+                const long long row = (long long)r * c.psz + (meta_at[warp][m & 63] & ~15);
+                const bool on = pg >= 0;
+                const long long p = on ? pg : 0;
+                const uint8_t* kc = c.kc + p * c.kcp + row * (D / 2);
+                const uint8_t* vc = c.vc + p * c.vcp + row * (D / 2);
+                const uint32_t dst = ring_a + (m % kStages) * St::BYTES;
+                auto cp = [&](uint32_t d, const uint8_t* src) {
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(d), "l"(src), "r"(on ? 16 : 0));
+                };
+#pragma unroll
+                for (int k = 0; k < St::CODES / 512; ++k) {
+                    const int pc = lane + 32 * k;
+                    cp(dst + St::K + pc * 16, kc + pc * 16);
+                    // 16-byte pieces 0, 1 and 2, 3 of a value row change places in rows 2, 3, 6, 7, ...
+                    const int vp = D == 128 ? pc ^ (((pc >> 3) & 1) << 1) : pc;
+                    cp(dst + St::V + vp * 16, vc + pc * 16);
+                }
+                constexpr int SP = St::SCALES / 16;
+                if (lane < SP) cp(dst + St::KS + lane * 16, c.ks + p * c.ksp + row * NG + lane * 16);
+                else if (lane < 2 * SP)
+                    cp(dst + St::VS + (lane - SP) * 16, c.vs + p * c.vsp + row * NG + (lane - SP) * 16);
+            }
+            cp_async_commit();
+        };
+        fetch(0);
+        publish(0);
+#pragma unroll
+        for (int k = 0; k < kStages - 1; ++k) issue(k);
+
+        // ---- the query: operand B of S^T (columns = heads), in the order of the key words ------------
+        uint32_t qf[NT][NG][4];
+        float off[NT][NG][2];   // -136 sum(q) of each scale group, heads 2 t4 and 2 t4 + 1
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int h = nt * 8 + g;
+#pragma unroll
+            for (int gg = 0; gg < NG; ++gg) {
+                uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+                if (h < G)
+                    raw = *reinterpret_cast<const uint4*>(a.q + ((long long)b * s.hq + r * G + h) * D + gg * kGrp + t4 * 8);
+                // elements (0,4), (1,5), (2,6), (3,7)
+                qf[nt][gg][0] = __byte_perm(raw.x, raw.z, 0x5410);
+                qf[nt][gg][1] = __byte_perm(raw.x, raw.z, 0x7632);
+                qf[nt][gg][2] = __byte_perm(raw.y, raw.w, 0x5410);
+                qf[nt][gg][3] = __byte_perm(raw.y, raw.w, 0x7632);
+                float v[8], sum = 0.f;
+                Vec<__nv_bfloat16>::cvt(raw, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum += v[e];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);   // over t4: head g's sum
+                off[nt][gg][0] = -136.f * __shfl_sync(0xffffffffu, sum, 8 * t4);
+                off[nt][gg][1] = -136.f * __shfl_sync(0xffffffffu, sum, 8 * t4 + 4);
+            }
+        }
+        float o[NT][MT][4], ref[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            ref[nt][0] = ref[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) o[nt][m][0] = o[nt][m][1] = o[nt][m][2] = o[nt][m][3] = 0.f;
+        }
+
+        for (int m = 0; m < nm; ++m) {
+            if ((m & 31) == 0) fetch(m + 32);
+            if ((m & 31) == 16) publish(m + 16);
+            cp_async_wait<kStages - 2>();
+            __syncwarp();
+            issue(m + kStages - 1);
+            const char* stg = ring + (m % kStages) * St::BYTES;
+            const int nv = (meta_at[warp][m & 63] & 15) + 1;
+            const float bias2 = meta_b[warp][m & 63];
+
+            // ---- S^T ---------------------------------------------------------------------------------
+            uint32_t ka[NG], kb[NG], sa, sb;
+            if constexpr (D == 128) {
+                const uint4 u = *reinterpret_cast<const uint4*>(stg + St::K + tk * 64 + t4 * 16);
+                const uint4 v = *reinterpret_cast<const uint4*>(stg + St::K + (tk + 8) * 64 + t4 * 16);
+                ka[0] = u.x; ka[1] = u.y; ka[2] = u.z; ka[3] = u.w;
+                kb[0] = v.x; kb[1] = v.y; kb[2] = v.z; kb[3] = v.w;
+                sa = *reinterpret_cast<const uint32_t*>(stg + St::KS + tk * 4);
+                sb = *reinterpret_cast<const uint32_t*>(stg + St::KS + (tk + 8) * 4);
+            } else {
+                const uint2 u = *reinterpret_cast<const uint2*>(stg + St::K + tk * 32 + t4 * 8);
+                const uint2 v = *reinterpret_cast<const uint2*>(stg + St::K + (tk + 8) * 32 + t4 * 8);
+                ka[0] = u.x; ka[1] = u.y;
+                kb[0] = v.x; kb[1] = v.y;
+                sa = *reinterpret_cast<const uint16_t*>(stg + St::KS + tk * 2);
+                sb = *reinterpret_cast<const uint16_t*>(stg + St::KS + (tk + 8) * 2);
+            }
+            float z[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) z[nt][0] = z[nt][1] = z[nt][2] = z[nt][3] = 0.f;
+#pragma unroll
+            for (int gg = 0; gg < NG; gg += 2) {
+                const float2 fa = __half22float2(h2(e4m3x2_to_f16x2(sa >> (8 * gg))));
+                const float2 fb = __half22float2(h2(e4m3x2_to_f16x2(sb >> (8 * gg))));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t w = ka[gg + e], v = kb[gg + e];
+                    const uint32_t a0[4] = {k_pair(w, 0), k_pair(v, 0), k_pair(w, 1), k_pair(v, 1)};
+                    const uint32_t a1[4] = {k_pair(w, 2), k_pair(v, 2), k_pair(w, 3), k_pair(v, 3)};
+                    const float fae = e ? fa.y : fa.x, fbe = e ? fb.y : fb.x;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float d[4] = {off[nt][gg + e][0], off[nt][gg + e][1], off[nt][gg + e][0], off[nt][gg + e][1]};
+                        mma_bf16(d, a0, qf[nt][gg + e][0], qf[nt][gg + e][1]);
+                        mma_bf16(d, a1, qf[nt][gg + e][2], qf[nt][gg + e][3]);
+                        z[nt][0] = fmaf(fae, d[0], z[nt][0]);
+                        z[nt][1] = fmaf(fae, d[1], z[nt][1]);
+                        z[nt][2] = fmaf(fbe, d[2], z[nt][2]);
+                        z[nt][3] = fmaf(fbe, d[3], z[nt][3]);
+                    }
+                }
+            }
+            bool over = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[nt][e] = fmaf(z[nt][e], scale2, bias2);
+                if (nv < kGran) {   // the end of the query's own chunk
+                    if (tk >= nv) z[nt][0] = z[nt][1] = -INFINITY;
+                    if (tk + 8 >= nv) z[nt][2] = z[nt][3] = -INFINITY;
+                }
+                over = over || fmaxf(z[nt][0], z[nt][2]) > ref[nt][0] + 6.f || fmaxf(z[nt][1], z[nt][3]) > ref[nt][1] + 6.f;
+            }
+            if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(z[nt][e], z[nt][e + 2]);
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        mx = fmaxf(mx, ref[nt][e]);
+                        const float cr = mx == -INFINITY ? 1.f : exp2f(ref[nt][e] - mx);
+                        ref[nt][e] = mx;
+                        l[nt][e] *= cr;
+#pragma unroll
+                        for (int k = 0; k < MT; ++k) { o[nt][k][e] *= cr; o[nt][k][e + 2] *= cr; }
+                    }
+            }
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float r0 = ref[nt][0] == -INFINITY ? 0.f : ref[nt][0], r1 = ref[nt][1] == -INFINITY ? 0.f : ref[nt][1];
+                const float q0 = exp2f(z[nt][0] - r0), q1 = exp2f(z[nt][1] - r1);
+                const float q2 = exp2f(z[nt][2] - r0), q3 = exp2f(z[nt][3] - r1);
+                l[nt][0] += q0 + q2;
+                l[nt][1] += q1 + q3;
+                pb[nt][0] = movm_t(pack_f16(q0, q1));
+                pb[nt][1] = movm_t(pack_f16(q2, q3));
+            }
+
+            // ---- O^T ---------------------------------------------------------------------------------
+            uint32_t vw[4][NW], s01, s23;
+            {
+                const int rows[4] = {vr0, vr1, vr0 + 8, vr1 + 8};
+                uint32_t sc[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int rw = rows[k];
+                    if constexpr (D == 128) {
+                        const int pc = (g >> 1) ^ (((rw >> 1) & 1) << 1);
+                        const uint2 u = *reinterpret_cast<const uint2*>(stg + St::V + rw * 64 + pc * 16 + (g & 1) * 8);
+                        vw[k][0] = u.x; vw[k][1] = u.y;
+                        sc[k] = *reinterpret_cast<const uint8_t*>(stg + St::VS + rw * 4 + (g >> 1));
+                    } else {
+                        vw[k][0] = *reinterpret_cast<const uint32_t*>(stg + St::V + rw * 32 + g * 4);
+                        sc[k] = *reinterpret_cast<const uint8_t*>(stg + St::VS + rw * 2 + (g >> 2));
+                    }
+                    if (rw >= nv) sc[k] = 0;   // beyond the query: whatever the page holds counts as 0
+                }
+                s01 = e4m3x2_to_f16x2(sc[0] | sc[1] << 8);
+                s23 = e4m3x2_to_f16x2(sc[2] | sc[3] << 8);
+            }
+            // multipliers and offsets of the two code positions, for rows (vr0, vr1) and (+8)
+            const __half2 sx = __hmul2(h2(s01), __float2half2_rn(0.0625f)), sy = __hmul2(h2(s23), __float2half2_rn(0.0625f));
+            const __half2 lx = __hmul2(sx, __float2half2_rn(-1032.f)), ly = __hmul2(sy, __float2half2_rn(-1032.f));
+            const __half2 hx = __hmul2(sx, __float2half2_rn(-72.f)), hy = __hmul2(sy, __float2half2_rn(-72.f));
+            const __half2 tx = __hmul2(sx, __float2half2_rn(0.0625f)), ty = __hmul2(sy, __float2half2_rn(0.0625f));
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                uint32_t xl = __byte_perm(vw[0][w], vw[1][w], 0x5410), xh = __byte_perm(vw[0][w], vw[1][w], 0x7632);
+                uint32_t yl = __byte_perm(vw[2][w], vw[3][w], 0x5410), yh = __byte_perm(vw[2][w], vw[3][w], 0x7632);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t mask = k & 1 ? 0x00f000f0u : 0x000f000fu;
+                    const __half2 mx = k & 1 ? tx : sx, ax = k & 1 ? hx : lx, my = k & 1 ? ty : sy, ay = k & 1 ? hy : ly;
+                    const uint32_t f[4] = {h2(__hfma2(h2((xl & mask) | 0x64006400u), mx, ax)),
+                                           h2(__hfma2(h2((xh & mask) | 0x64006400u), mx, ax)),
+                                           h2(__hfma2(h2((yl & mask) | 0x64006400u), my, ay)),
+                                           h2(__hfma2(h2((yh & mask) | 0x64006400u), my, ay))};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][w * 4 + k], f, pb[nt][0], pb[nt][1]);
+                    if (k == 1) { xl >>= 8; xh >>= 8; yl >>= 8; yh >>= 8; }
+                }
+            }
+        }
+
+        // ---- merge the warps (fixed order), each through its own drained ring -----------------------
+        cp_async_wait<0>();
+        __syncwarp();
+        float* ob = reinterpret_cast<float*>(ring);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float v = l[nt][e];
+                v += __shfl_xor_sync(0xffffffffu, v, 4);
+                v += __shfl_xor_sync(0xffffffffu, v, 8);
+                v += __shfl_xor_sync(0xffffffffu, v, 16);
+                if (g == 0) {
+                    mrg_m[warp][nt * 8 + 2 * t4 + e] = ref[nt][e];
+                    mrg_l[warp][nt * 8 + 2 * t4 + e] = v;
+                }
+#pragma unroll
+                for (int w = 0; w < NW; ++w)
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh)
+                        *reinterpret_cast<float4*>(ob + (nt * 8 + 2 * t4 + e) * OLD + (g * NW + w) * 8 + hh * 4) =
+                            make_float4(o[nt][w * 4][e + 2 * hh], o[nt][w * 4 + 1][e + 2 * hh],
+                                        o[nt][w * 4 + 2][e + 2 * hh], o[nt][w * 4 + 3][e + 2 * hh]);
+            }
+        }
+        __syncthreads();
+        if (threadIdx.x < 8 * NT) {
+            const int h = threadIdx.x;
+            float M = -INFINITY, sum = 0.f;
+            for (int w = 0; w < W; ++w) M = fmaxf(M, mrg_m[w][h]);
+            for (int w = 0; w < W; ++w) {
+                const float f = mrg_m[w][h] == -INFINITY ? 0.f : exp2f(mrg_m[w][h] - M);
+                mrg_s[w][h] = f;
+                // a warp without granules, or whose logits were all NaN, has no reference
+                sum += mrg_m[w][h] == -INFINITY ? mrg_l[w][h] : mrg_l[w][h] * f;
+            }
+            tot_m[h] = M;
+            tot_l[h] = sum;
+        }
+        __syncthreads();
+        const bool whole = s_lo == p0 && s_hi == p1;
+        float* pb = a.part + ((long long)blockIdx.x * 2 + (s_lo > p0 ? 0 : 1)) * G * (D + 2);
+        for (int v = threadIdx.x; v < G * (D / 4); v += 32 * W) {
+            const int h = v / (D / 4), dd = v % (D / 4) * 4;
+            float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int w = 0; w < W; ++w) {
+                const float f = mrg_s[w][h];
+                const float4 u = *reinterpret_cast<const float4*>(smem + w * (kStages * St::BYTES) + (h * OLD + dd) * 4);
+                t.x = fmaf(u.x, f, t.x); t.y = fmaf(u.y, f, t.y); t.z = fmaf(u.z, f, t.z); t.w = fmaf(u.w, f, t.w);
+            }
+            if (whole) {
+                const float inv = out_scale / tot_l[h];
+                uint2 res;
+                res.x = pack_bf16(t.x * inv, t.y * inv);
+                res.y = pack_bf16(t.z * inv, t.w * inv);
+                *reinterpret_cast<uint2*>(a.O + ((long long)b * s.hq + r * G + h) * D + dd) = res;
+            } else {
+                float* row = pb + h * (D + 2) + dd;   // rows of D + 2 floats: 8-byte aligned
+                *reinterpret_cast<float2*>(row) = make_float2(t.x, t.y);
+                *reinterpret_cast<float2*>(row + 2) = make_float2(t.z, t.w);
+            }
+        }
+        if (!whole && threadIdx.x < G) {
+            pb[threadIdx.x * (D + 2) + D] = tot_m[threadIdx.x];
+            pb[threadIdx.x * (D + 2) + D + 1] = tot_l[threadIdx.x];
+        }
+        __syncthreads();   // the rings and mrg_* are used again
+    }
+}
+
+// Pairs that span blocks (and zeros for empty sequences): one block per (pair, head) or per pair,
+// kMergeY partials at a time, weights first.
+constexpr int kMergeY = 8, kMaxBlocks = 1024;
+
+template <int D>
+__global__ void __launch_bounds__(D * kMergeY) q4_merge_kernel(Shape s, Attend a, int vexp)
+{
+    __shared__ float wt[kMaxBlocks], sums[kMaxBlocks], acc[kMergeY][D];
+    __shared__ float red[32];
+    pdl_wait();
+    const int x = blockIdx.x, G = s.g, BR = s.batch * s.hkv, col = threadIdx.x % D, y = threadIdx.x / D;
+    const int b = x / s.hkv, r = x % s.hkv;
+    const int p0 = a.pre[x], p1 = a.pre[x + 1], used = a.pre[BR + 1];
+    const long long total = a.pre[BR];
+    __nv_bfloat16* out = a.O + ((long long)b * s.hq + r * G) * D;
+    if (p0 == p1) {
+        for (int h = blockIdx.y; h < G; h += gridDim.y)
+            if (y == 0) out[h * D + col] = __float2bfloat16_rn(0.f);
+        return;
+    }
+    auto at = [&](int c) { return (int)(total * c / used); };
+    auto block_of = [&](int k) {   // the block whose range holds granule k
+        int c = (int)((long long)k * used / total);
+        while (c > 0 && at(c) > k) --c;
+        while (c + 1 < used && at(c + 1) <= k) ++c;
+        return c;
+    };
+    const int c0 = block_of(p0), c1 = block_of(p1 - 1), n = c1 - c0 + 1;
+    if (n == 1) return;   // finished in its block
+    const long long stride = (long long)G * (D + 2);
+    for (int h = blockIdx.y; h < G; h += gridDim.y) {
+        // partial j: the last piece of block c0 (j = 0), the first piece of block c0 + j
+        const float* base = a.part + (long long)h * (D + 2);
+        auto piece = [&](int j) { return base + ((long long)(c0 + j) * 2 + (j == 0 ? 1 : 0)) * stride; };
+        float M = -INFINITY;
+        for (int j = threadIdx.x; j < n; j += D * kMergeY) {
+            const float* p = piece(j);
+            wt[j] = p[D];
+            sums[j] = p[D + 1];
+            M = fmaxf(M, wt[j]);
+        }
+        M = warp_max(M);
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = M;
+        __syncthreads();
+        M = -INFINITY;
+        for (int w = 0; w < D * kMergeY / 32; ++w) M = fmaxf(M, red[w]);
+        for (int j = threadIdx.x; j < n; j += D * kMergeY) wt[j] = wt[j] == -INFINITY ? 0.f : exp2f(wt[j] - M);
+        __syncthreads();
+        float t = 0.f;
+        int j = y;
+        for (; j + 3 * kMergeY < n; j += 4 * kMergeY) {
+            float v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[u] = piece(j + u * kMergeY)[col];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) t = fmaf(v[u], wt[j + u * kMergeY], t);
+        }
+        for (; j < n; j += kMergeY) t = fmaf(piece(j)[col], wt[j], t);
+        acc[y][col] = t;
+        __syncthreads();
+        if (y == 0) {
+            float sum = 0.f;
+            for (int k = 0; k < n; ++k) sum = fmaf(sums[k], wt[k], sum);
+            t = 0.f;
+            for (int k = 0; k < kMergeY; ++k) t += acc[k][col];
+            out[h * D + col] = __float2bfloat16_rn(t * (16.f * exp2i(vexp)) / sum);
+        }
+        __syncthreads();
+    }
+}
+
+template <int D, int NT>
+cudaError_t attend_t(const Shape& s, const Q4& c, const Routes& rt, const Attend& a, cudaStream_t st)
+{
+    auto k = q4_attend_kernel<D, NT>;
+    const size_t smem = (size_t)Cfg<NT>::W * kStages * Stage<D>::BYTES;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    e = launch_after(k, dim3(dec_tma_blocks()), dim3(32 * Cfg<NT>::W), smem, st, s, c, rt, a);
+    if (e != cudaSuccess) return e;
+    const int pairs = s.batch * s.hkv;
+    return launch_after(q4_merge_kernel<D>, dim3(pairs, pairs * s.g <= 1024 ? s.g : 1), dim3(D * kMergeY), 0, st, s, a, c.vexp);
+}
+
+}  // namespace
+
+int q4_max_pairs() { return kMaxPairs; }
+
+size_t q4_part_floats(const Shape& s) { return (size_t)dec_tma_blocks() * 2 * s.g * (s.d + 2); }
+
+cudaError_t launch_attend_q4(const Shape& s, const Q4& c, const void* q, const int* seqlens, const Routes& rt, bool dense,
+                             float* part, int* pre, void* O, cudaStream_t st)
+{
+    const Attend a{(const __nv_bfloat16*)q, seqlens, dense ? 1 : 0, part, pre, (__nv_bfloat16*)O};
+    if (s.d == 128) return s.g <= 8 ? attend_t<128, 1>(s, c, rt, a, st) : attend_t<128, 2>(s, c, rt, a, st);
+    return s.g <= 8 ? attend_t<64, 1>(s, c, rt, a, st) : attend_t<64, 2>(s, c, rt, a, st);
+}
+
+}  // namespace dash
