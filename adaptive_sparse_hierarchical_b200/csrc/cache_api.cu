@@ -12,7 +12,7 @@ cudaError_t launch_append_q4(const Shape& s, const Q4& c, const void* K, const v
 cudaError_t launch_load_q4(const Shape& s, const Q4& c, const int* start, int offset, int n, const int* seqlens,
                            void* K, void* V, cudaStream_t st);
 cudaError_t launch_attend_q4(const Shape& s, const Q4& c, const void* q, const int* seqlens, const Routes& rt, bool dense,
-                             float* part, int* pre, void* O, cudaStream_t st);
+                             float* part, int* span, void* O, cudaStream_t st);
 int q4_max_pairs();
 size_t q4_part_floats(const Shape& s);
 
@@ -75,15 +75,15 @@ Q4 cache_of(const dash_q4_kv* kv)
     return c;
 }
 
-struct Q4Layout { size_t part, pre, counts, idx, bias, x, err, total; };
+struct Q4Layout { size_t part, span, counts, idx, bias, x, err, total; };
 Q4Layout q4_layout(const dash_params* p)
 {
     Q4Layout L;
     const Shape s = shape_of(p);
     const size_t bh = (size_t)s.batch * s.hkv, T = s.T > 0 ? s.T : 1;
     L.part = 0;
-    L.pre = L.part + up(q4_part_floats(s) * 4);
-    L.counts = L.pre + up((bh + 2) * 4);
+    L.span = L.part + up(q4_part_floats(s) * 4);
+    L.counts = L.span + up(bh * 8);
     L.idx = L.counts + up(bh * 4);
     L.bias = L.idx + up(bh * T * 4);
     L.x = L.bias + up(bh * T * 4);
@@ -195,7 +195,7 @@ int dash_decode_q4(const dash_params* p, const dash_q4_kv* kv, const void* q, co
                                            (int*)(ws + L.err), (cudaStream_t)stream));
         if (rc != DASH_OK) return rc;
     }
-    return status_of(launch_attend_q4(s, cache_of(kv), q, seqlens, rt, dense, (float*)(ws + L.part), (int*)(ws + L.pre), O,
+    return status_of(launch_attend_q4(s, cache_of(kv), q, seqlens, rt, dense, (float*)(ws + L.part), (int*)(ws + L.span), O,
                                       (cudaStream_t)stream));
 }
 

@@ -13,10 +13,13 @@
 //
 // A warp computes S^T = K q^T and O^T = V^T P^T: the 16 tokens (then 16 of the d_h elements) are the
 // 16 rows of m16n8k16 MMAs and the heads the 8 columns, so groups of up to 8 heads fill the tile.
-//   K: the operand is 128 + u (bf16, one mask-or per two codes), straight from a 16-byte load: key
-//      rows are stored in the order of the operand's registers.  The accumulator starts at
-//      -136 sum(q) over the scale group, which takes the offset off, and each group's sum is
-//      multiplied by the key's scale in fp32: the codes enter the product exactly.
+//   K: the f16 number with the bits of a code u in its lowest bits is u 2^-24, in the next four 16 u
+//      2^-24 (subnormals: linear, and exact in the MMA): two masks, a shift and two masks turn a word
+//      of 8 codes into operands, straight from a 16-byte load (key rows are stored in the operand's
+//      order).  The query, scaled by a power of two to have its largest element in 2^14..2^15, is
+//      exact in f16 (its elements for the upper masks divided by 16) down to 2^-27 of the largest.
+//      Each scale group's sum is multiplied by the key's scale in fp32.  The codes' offset of 8 is one
+//      more MMA: the tokens' scales times -8 sum(q) of each group (two f16 numbers, 22 bits).
 //   V: the operand needs the scale inside the sum over tokens.  1024 + u (or 1024 + 16 u) in f16,
 //      one f16x2 fma (1024 + u) s' - 1032 s' gives (u - 8) s' exactly: with s' = scale / 16,
 //      1032 s' has at most 8 + 4 - 1 = 11 significant bits (129 * 15 < 2^11) and is below 2^15.
@@ -39,6 +42,13 @@ constexpr int kStages = 4;
 constexpr int kMaxPairs = 2048;
 constexpr int kMeta = 64;         // granule descriptors per warp (two halves of 32)
 
+// Descriptor of a granule: where its codes and scales lie, its chunk's bias, tokens | mapped << 8.
+struct Meta {
+    ulonglong2 kv[kMeta], sc[kMeta];
+    float bias[kMeta];
+    int nv[kMeta];
+};
+
 // Warps per block: one block per SM, as many warps as the registers of NT head tiles allow.
 template <int NT> struct Cfg { static constexpr int W = NT == 1 ? 16 : 12; };
 
@@ -54,7 +64,7 @@ struct Attend {
     const int* seqlens;
     int dense;        // every chunk before the query's own, bias 0 (no route lists)
     float* part;      // [block][first, last][g][D + 2]: partial o, reference, sum
-    int* pre;         // [pairs + 2]: granules before each pair, total, blocks in use
+    int2* span;       // [pairs]: first and last block of each pair (0, -1: no granules)
     __nv_bfloat16* O;
 };
 
@@ -64,6 +74,30 @@ __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0
                  "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t h2(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
+__device__ __forceinline__ __half2 h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
+// (x & MASK) | magic in one instruction (written in C with two constants it becomes two)
+template <uint32_t MASK>
+__device__ __forceinline__ __half2 pick(uint32_t x, uint32_t magic)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "n"(MASK), "r"(magic));
+    return h2(r);
+}
+// d = a b
+__device__ __forceinline__ void mma_f16_0(float* d, const uint32_t* a, uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+                 "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 __device__ __forceinline__ uint32_t movm_t(uint32_t x)
 {
@@ -76,12 +110,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ uint32_t h2(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
-__device__ __forceinline__ __half2 h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
-
-// 128 + code i and 128 + code i + 4 of a word, as bf16x2
-__device__ __forceinline__ uint32_t k_pair(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u; }
-
 // Token (row of the granule) behind row m < 8 of S^T (row m + 8: the same + 8).  Even rows 0..3 and
 // odd rows 5, 4, 7, 6: keys read two rows of opposite parity at once, values rows 0..3 or 4..7,
 // which the swizzle of the value rows spreads over all banks.
@@ -99,8 +127,6 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, 
     extern __shared__ __align__(128) char smem[];
     __shared__ int pre[kMaxPairs + 1];
     __shared__ float mrg_m[W][8 * NT], mrg_l[W][8 * NT], mrg_s[W][8 * NT], tot_m[8 * NT], tot_l[8 * NT];
-    __shared__ int meta_pg[W][kMeta], meta_at[W][kMeta];
-    __shared__ float meta_b[W][kMeta];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int BR = s.batch * s.hkv, G = s.g, NB = s.B / kGran;
@@ -130,19 +156,28 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, 
     const long long total = pre[BR];
     // every warp of a block in use has a granule
     const int used = (int)min((long long)gridDim.x, (total + W - 1) / W);
-    if (blockIdx.x == 0) {
-        for (int x = threadIdx.x; x <= BR; x += 32 * W) a.pre[x] = pre[x];
-        if (threadIdx.x == 0) a.pre[BR + 1] = used;
-    }
+    if (blockIdx.x == 0)
+        for (int x = threadIdx.x; x < BR; x += 32 * W)
+            if (pre[x] == pre[x + 1]) a.span[x] = make_int2(0, -1);
     if ((int)blockIdx.x >= used) return;
     const int lo = (int)(total * blockIdx.x / used), hi = (int)(total * (blockIdx.x + 1) / used);
 
     char* ring = smem + warp * (kStages * St::BYTES);
     const uint32_t ring_a = smem_u32(ring);
-    const float scale2 = kLog2e * rsqrtf((float)D) * exp2i(c.kexp);
+    Meta& meta = *reinterpret_cast<Meta*>(smem + W * kStages * St::BYTES + warp * sizeof(Meta));
+    // the operands carry the codes times 2^-24
+    const float scale2 = kLog2e * rsqrtf((float)D) * exp2i(c.kexp) * 16777216.f;
     const float out_scale = 16.f * exp2i(c.vexp);
+    uint32_t magic = 0x64006400u;                    // 1024, 1024 in f16
+    asm volatile("" : "+r"(magic));                  // kept in a register
     const int tk = tok_of(g);                        // this lane's key rows: tk, tk + 8
     const int vr0 = t4, vr1 = (t4 ^ 1) + 4;          // its value rows: vr0, vr1, vr0 + 8, vr1 + 8
+    // places of its words and scales in a stage (16-byte pieces of value rows are swizzled, see issue())
+    auto v_at = [&](int row) {
+        return St::V + (D == 128 ? row * 64 + ((g >> 1) ^ (((row >> 1) & 1) << 1)) * 16 + (g & 1) * 8 : row * 32 + g * 4);
+    };
+    const int vw0 = v_at(vr0), vw1 = v_at(vr1);
+    const int vs0 = St::VS + vr0 * NG + (D == 128 ? g >> 1 : g >> 2), vs1 = St::VS + vr1 * NG + (D == 128 ? g >> 1 : g >> 2);
 
     int x = 0;
     {   // first pair with granules in this block's range
@@ -163,8 +198,9 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, 
         const int nm = max(0, (s_hi - s_lo - warp + W - 1) / W);
 
         // ---- granule descriptors, 32 at a time (page, row and number of tokens, bias) ----------------
-        int f_pg = -1, f_at = 0;
+        ulonglong2 f_kv = {}, f_sc = {};
         float f_b = 0.f;
+        int f_nv = 0;
         auto fetch = [&](int m0) {
             const int m = m0 + lane;
             if (m >= nm) return;
@@ -182,73 +218,105 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, 
                 tok = (i / s.B) * s.B + (t - full) * kGran;
                 nv = min(kGran, i + 1 - tok);
             }
-            f_pg = q4_page(c, b, tok);
-            f_at = tok % c.psz | (nv - 1);   // rows of granules are multiples of 16
+            const int pg = q4_page(c, b, tok);
+            const long long p = pg >= 0 ? pg : 0, row = (long long)r * c.psz + tok % c.psz;
+            f_kv.x = (unsigned long long)(c.kc + p * c.kcp + row * (D / 2));
+            f_kv.y = (unsigned long long)(c.vc + p * c.vcp + row * (D / 2));
+            f_sc.x = (unsigned long long)(c.ks + p * c.ksp + row * NG);
+            f_sc.y = (unsigned long long)(c.vs + p * c.vsp + row * NG);
+            f_nv = nv | (pg >= 0 ? 1 << 8 : 0);
         };
         auto publish = [&](int m0) {
             const int k = (m0 & 32) + lane;
-            meta_pg[warp][k] = f_pg;
-            meta_at[warp][k] = f_at;
-            meta_b[warp][k] = f_b;
+            meta.kv[k] = f_kv;
+            meta.sc[k] = f_sc;
+            meta.bias[k] = f_b;
+            meta.nv[k] = f_nv;
             __syncwarp();
         };
-        auto issue = [&](int m) {
+        constexpr int SP = St::SCALES / 16;
+        const int lane16 = lane * 16, vlane16 = D == 128 ? (lane ^ (((lane >> 3) & 1) << 1)) * 16 : lane16;
+        auto issue = [&](int m, uint32_t dst) {
             if (m < nm) {
-                const int pg = meta_pg[warp][m & 63];
-                const long long row = (long long)r * c.psz + (meta_at[warp][m & 63] & ~15);
-                const bool on = pg >= 0;
-                const long long p = on ? pg : 0;
-                const uint8_t* kc = c.kc + p * c.kcp + row * (D / 2);
-                const uint8_t* vc = c.vc + p * c.vcp + row * (D / 2);
-                const uint32_t dst = ring_a + (m % kStages) * St::BYTES;
-                auto cp = [&](uint32_t d, const uint8_t* src) {
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(d), "l"(src), "r"(on ? 16 : 0));
-                };
-#pragma unroll
-                for (int k = 0; k < St::CODES / 512; ++k) {
-                    const int pc = lane + 32 * k;
-                    cp(dst + St::K + pc * 16, kc + pc * 16);
-                    // 16-byte pieces 0, 1 and 2, 3 of a value row change places in rows 2, 3, 6, 7, ...
-                    const int vp = D == 128 ? pc ^ (((pc >> 3) & 1) << 1) : pc;
-                    cp(dst + St::V + vp * 16, vc + pc * 16);
-                }
-                constexpr int SP = St::SCALES / 16;
-                if (lane < SP) cp(dst + St::KS + lane * 16, c.ks + p * c.ksp + row * NG + lane * 16);
-                else if (lane < 2 * SP)
-                    cp(dst + St::VS + (lane - SP) * 16, c.vs + p * c.vsp + row * NG + (lane - SP) * 16);
+                const int k = m & (kMeta - 1);
+                const ulonglong2 kv = meta.kv[k];
+                const unsigned long long sc = reinterpret_cast<const unsigned long long*>(&meta.sc[k])[(lane / SP) & 1];
+                // 16-byte pieces 0, 1 and 2, 3 of a value row change places in rows 2, 3, 6, 7, ...; the value
+                // scales follow the key scales in the stage; zeros where the page is not mapped
+                if constexpr (D == 128)
+                    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.lt.s32 p, %5, 256;\n\tsetp.ne.s32 q, %7, 0;\n\t"
+                                 "cp.async.cg.shared.global [%0], [%2], 16, p;\n\t"
+                                 "cp.async.cg.shared.global [%0 + 512], [%2 + 512], 16, p;\n\t"
+                                 "cp.async.cg.shared.global [%1 + 1024], [%3], 16, p;\n\t"
+                                 "cp.async.cg.shared.global [%1 + 1536], [%3 + 512], 16, p;\n\t"
+                                 "@q cp.async.cg.shared.global [%0 + %6], [%4], 16, p;\n\t}\n" ::"r"(dst + lane16),
+                                 "r"(dst + vlane16), "l"(kv.x + lane16), "l"(kv.y + lane16),
+                                 "l"(sc + lane16 % (SP * 16)), "r"(meta.nv[k]), "n"(St::KS), "r"((int)(lane < 2 * SP)));
+                else
+                    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.lt.s32 p, %5, 256;\n\tsetp.ne.s32 q, %7, 0;\n\t"
+                                 "cp.async.cg.shared.global [%0], [%2], 16, p;\n\t"
+                                 "cp.async.cg.shared.global [%1 + 512], [%3], 16, p;\n\t"
+                                 "@q cp.async.cg.shared.global [%0 + %6], [%4], 16, p;\n\t}\n" ::"r"(dst + lane16),
+                                 "r"(dst + vlane16), "l"(kv.x + lane16), "l"(kv.y + lane16),
+                                 "l"(sc + lane16 % (SP * 16)), "r"(meta.nv[k]), "n"(St::KS), "r"((int)(lane < 2 * SP)));
             }
             cp_async_commit();
         };
         fetch(0);
         publish(0);
 #pragma unroll
-        for (int k = 0; k < kStages - 1; ++k) issue(k);
+        for (int k = 0; k < kStages - 1; ++k) issue(k, ring_a + k * St::BYTES);
 
         // ---- the query: operand B of S^T (columns = heads), in the order of the key words ------------
-        uint32_t qf[NT][NG][4];
-        float off[NT][NG][2];   // -136 sum(q) of each scale group, heads 2 t4 and 2 t4 + 1
+        uint32_t qf[NT][NG][4];   // elements (0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16 of the lane's word
+        uint32_t qs[NT];          // -2^-13 sum(q) of groups 2 (t4 % 2) and + 1: rounded to f16, and the rest
+        float fac[NT][2];         // logit per accumulated unit of heads 2 t4 and 2 t4 + 1
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int h = nt * 8 + g;
+            uint4 raw[NG];
+            uint32_t top = 0;
 #pragma unroll
             for (int gg = 0; gg < NG; ++gg) {
-                uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+                raw[gg] = make_uint4(0u, 0u, 0u, 0u);
                 if (h < G)
-                    raw = *reinterpret_cast<const uint4*>(a.q + ((long long)b * s.hq + r * G + h) * D + gg * kGrp + t4 * 8);
-                // elements (0,4), (1,5), (2,6), (3,7)
-                qf[nt][gg][0] = __byte_perm(raw.x, raw.z, 0x5410);
-                qf[nt][gg][1] = __byte_perm(raw.x, raw.z, 0x7632);
-                qf[nt][gg][2] = __byte_perm(raw.y, raw.w, 0x5410);
-                qf[nt][gg][3] = __byte_perm(raw.y, raw.w, 0x7632);
-                float v[8], sum = 0.f;
-                Vec<__nv_bfloat16>::cvt(raw, v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum += v[e];
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);   // over t4: head g's sum
-                off[nt][gg][0] = -136.f * __shfl_sync(0xffffffffu, sum, 8 * t4);
-                off[nt][gg][1] = -136.f * __shfl_sync(0xffffffffu, sum, 8 * t4 + 4);
+                    raw[gg] = *reinterpret_cast<const uint4*>(a.q + ((long long)b * s.hq + r * G + h) * D + gg * kGrp + t4 * 8);
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[gg].x & 0x7fff7fffu, raw[gg].y & 0x7fff7fffu),
+                                             __vmaxu2(raw[gg].z & 0x7fff7fffu, raw[gg].w & 0x7fff7fffu)));
             }
+            top = max(top & 0xffffu, top >> 16);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // the power of two; a head with a NaN or an infinity becomes NaN as a whole
+            const int ce = min(141 - (int)(top >> 7), 120);
+            const float up = top >= 0x7f80u ? __int_as_float(0x7fffffff) : exp2i(ce);
+            const float down = scale2 * exp2i(-ce);
+            fac[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t4);
+            fac[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t4 + 4);
+            float sum[NG];
+#pragma unroll
+            for (int gg = 0; gg < NG; ++gg) {
+                float v[8];
+                Vec<__nv_bfloat16>::cvt(raw[gg], v);
+                sum[gg] = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[gg] += v[e] * up;
+                sum[gg] += __shfl_xor_sync(0xffffffffu, sum[gg], 1);
+                sum[gg] += __shfl_xor_sync(0xffffffffu, sum[gg], 2);   // over t4: head g's sum
+                const float up16 = up * 0.0625f;
+                qf[nt][gg][0] = pack_f16(v[0] * up, v[4] * up);
+                qf[nt][gg][1] = pack_f16(v[1] * up16, v[5] * up16);
+                qf[nt][gg][2] = pack_f16(v[2] * up, v[6] * up);
+                qf[nt][gg][3] = pack_f16(v[3] * up16, v[7] * up16);
+            }
+            // rows of the offset's operand: D = 128 has the rounded sums in lanes t4 = 0, 1 and the rests in
+            // t4 = 2, 3; D = 64 in t4 = 0 and t4 = 1
+            const bool second = D == 128 && (t4 & 1), rest = D == 128 ? t4 >= 2 : t4 == 1;
+            const float x0 = -0.0001220703125f * (second ? sum[NG - 2] : sum[0]);
+            const float x1 = -0.0001220703125f * (second ? sum[NG - 1] : sum[1]);
+            const uint32_t hi = pack_f16(x0, x1);
+            const float2 hf = __half22float2(h2(hi));
+            qs[nt] = rest ? pack_f16(x0 - hf.x, x1 - hf.y) : D == 128 || t4 == 0 ? hi : 0u;
         }
         float o[NT][MT][4], ref[NT][2], l[NT][2];
 #pragma unroll
@@ -259,15 +327,18 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, 
             for (int m = 0; m < MT; ++m) o[nt][m][0] = o[nt][m][1] = o[nt][m][2] = o[nt][m][3] = 0.f;
         }
 
+        uint32_t cur = 0, nxt = (kStages - 1) * St::BYTES;   // ring offsets of granule m and of the one to load
         for (int m = 0; m < nm; ++m) {
             if ((m & 31) == 0) fetch(m + 32);
             if ((m & 31) == 16) publish(m + 16);
             cp_async_wait<kStages - 2>();
             __syncwarp();
-            issue(m + kStages - 1);
-            const char* stg = ring + (m % kStages) * St::BYTES;
-            const int nv = (meta_at[warp][m & 63] & 15) + 1;
-            const float bias2 = meta_b[warp][m & 63];
+            issue(m + kStages - 1, ring_a + nxt);
+            const char* stg = ring + cur;
+            nxt = cur;
+            cur = cur == (kStages - 1) * St::BYTES ? 0 : cur + St::BYTES;
+            const int nv = meta.nv[m & (kMeta - 1)] & 255;
+            const float bias2 = meta.bias[m & (kMeta - 1)];
 
             // ---- S^T ---------------------------------------------------------------------------------
             uint32_t ka[NG], kb[NG], sa, sb;
@@ -286,54 +357,67 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, 
                 sa = *reinterpret_cast<const uint16_t*>(stg + St::KS + tk * 2);
                 sb = *reinterpret_cast<const uint16_t*>(stg + St::KS + (tk + 8) * 2);
             }
+            uint32_t fa[NG / 2], fb[NG / 2];   // scales of this lane's two tokens, f16x2
+#pragma unroll
+            for (int k = 0; k < NG / 2; ++k) {
+                fa[k] = e4m3x2_to_f16x2(sa >> (16 * k));
+                fb[k] = e4m3x2_to_f16x2(sb >> (16 * k));
+            }
             float z[NT][4];
+            {
+                const uint32_t ua = (t4 & 1) ? fa[NG / 2 - 1] : fa[0], ub = (t4 & 1) ? fb[NG / 2 - 1] : fb[0];
+                const __half2 e8 = __float2half2_rn(0.00390625f);   // 2^-8: with the sums' 2^-13, 8 times the codes' 2^-24
+                const uint32_t f[4] = {h2(__hmul2(h2(ua), e8)), h2(__hmul2(h2(ub), e8)), 0u, 0u};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) z[nt][0] = z[nt][1] = z[nt][2] = z[nt][3] = 0.f;
+                for (int nt = 0; nt < NT; ++nt) mma_f16_0(z[nt], f, qs[nt], 0u);
+            }
 #pragma unroll
-            for (int gg = 0; gg < NG; gg += 2) {
-                const float2 fa = __half22float2(h2(e4m3x2_to_f16x2(sa >> (8 * gg))));
-                const float2 fb = __half22float2(h2(e4m3x2_to_f16x2(sb >> (8 * gg))));
+            for (int gg = 0; gg < NG; ++gg) {
+                const uint32_t w = ka[gg], v = kb[gg], w8 = w >> 8, v8 = v >> 8;
+                const uint32_t f0[4] = {w & 0x000f000fu, v & 0x000f000fu, w & 0x00f000f0u, v & 0x00f000f0u};
+                const uint32_t f1[4] = {w8 & 0x000f000fu, v8 & 0x000f000fu, w8 & 0x00f000f0u, v8 & 0x00f000f0u};
+                const float2 pa = __half22float2(h2(fa[gg / 2])), pc = __half22float2(h2(fb[gg / 2]));
+                const float xa = gg & 1 ? pa.y : pa.x, xb = gg & 1 ? pc.y : pc.x;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t w = ka[gg + e], v = kb[gg + e];
-                    const uint32_t a0[4] = {k_pair(w, 0), k_pair(v, 0), k_pair(w, 1), k_pair(v, 1)};
-                    const uint32_t a1[4] = {k_pair(w, 2), k_pair(v, 2), k_pair(w, 3), k_pair(v, 3)};
-                    const float fae = e ? fa.y : fa.x, fbe = e ? fb.y : fb.x;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float d[4] = {off[nt][gg + e][0], off[nt][gg + e][1], off[nt][gg + e][0], off[nt][gg + e][1]};
-                        mma_bf16(d, a0, qf[nt][gg + e][0], qf[nt][gg + e][1]);
-                        mma_bf16(d, a1, qf[nt][gg + e][2], qf[nt][gg + e][3]);
-                        z[nt][0] = fmaf(fae, d[0], z[nt][0]);
-                        z[nt][1] = fmaf(fae, d[1], z[nt][1]);
-                        z[nt][2] = fmaf(fbe, d[2], z[nt][2]);
-                        z[nt][3] = fmaf(fbe, d[3], z[nt][3]);
-                    }
+                for (int nt = 0; nt < NT; ++nt) {
+                    float d[4];
+                    mma_f16_0(d, f0, qf[nt][gg][0], qf[nt][gg][1]);
+                    mma_f16(d, f1, qf[nt][gg][2], qf[nt][gg][3]);
+                    z[nt][0] = fmaf(xa, d[0], z[nt][0]);
+                    z[nt][1] = fmaf(xa, d[1], z[nt][1]);
+                    z[nt][2] = fmaf(xb, d[2], z[nt][2]);
+                    z[nt][3] = fmaf(xb, d[3], z[nt][3]);
                 }
             }
-            bool over = false;
+            // logits relative to the reference; before the first one it is -inf and they are +inf
+            float tz[NT][4], most = -INFINITY;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) z[nt][e] = fmaf(z[nt][e], scale2, bias2);
+                for (int e = 0; e < 4; ++e) tz[nt][e] = fmaf(z[nt][e], fac[nt][e & 1], bias2 - ref[nt][e & 1]);
                 if (nv < kGran) {   // the end of the query's own chunk
-                    if (tk >= nv) z[nt][0] = z[nt][1] = -INFINITY;
-                    if (tk + 8 >= nv) z[nt][2] = z[nt][3] = -INFINITY;
+                    if (tk >= nv) tz[nt][0] = tz[nt][1] = -INFINITY;
+                    if (tk + 8 >= nv) tz[nt][2] = tz[nt][3] = -INFINITY;
                 }
-                over = over || fmaxf(z[nt][0], z[nt][2]) > ref[nt][0] + 6.f || fmaxf(z[nt][1], z[nt][3]) > ref[nt][1] + 6.f;
+                most = fmaxf(most, fmaxf(fmaxf(tz[nt][0], tz[nt][1]), fmaxf(tz[nt][2], tz[nt][3])));
             }
-            if (__any_sync(0xffffffffu, over)) {
+            if (__any_sync(0xffffffffu, most > 6.f)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(z[nt][e], z[nt][e + 2]);
+                        float y0 = fmaf(z[nt][e], fac[nt][e], bias2), y1 = fmaf(z[nt][e + 2], fac[nt][e], bias2);
+                        if (tk >= nv) y0 = -INFINITY;
+                        if (tk + 8 >= nv) y1 = -INFINITY;
+                        float mx = fmaxf(y0, y1);
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                         mx = fmaxf(mx, ref[nt][e]);
-                        const float cr = mx == -INFINITY ? 1.f : exp2f(ref[nt][e] - mx);
+                        const float base = mx == -INFINITY ? 0.f : mx, cr = exp2f(ref[nt][e] - base);
                         ref[nt][e] = mx;
+                        tz[nt][e] = y0 - base;
+                        tz[nt][e + 2] = y1 - base;
                         l[nt][e] *= cr;
 #pragma unroll
                         for (int k = 0; k < MT; ++k) { o[nt][k][e] *= cr; o[nt][k][e + 2] *= cr; }
@@ -342,9 +426,7 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, 
             uint32_t pb[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float r0 = ref[nt][0] == -INFINITY ? 0.f : ref[nt][0], r1 = ref[nt][1] == -INFINITY ? 0.f : ref[nt][1];
-                const float q0 = exp2f(z[nt][0] - r0), q1 = exp2f(z[nt][1] - r1);
-                const float q2 = exp2f(z[nt][2] - r0), q3 = exp2f(z[nt][3] - r1);
+                const float q0 = ex2(tz[nt][0]), q1 = ex2(tz[nt][1]), q2 = ex2(tz[nt][2]), q3 = ex2(tz[nt][3]);
                 l[nt][0] += q0 + q2;
                 l[nt][1] += q1 + q3;
                 pb[nt][0] = movm_t(pack_f16(q0, q1));
@@ -354,22 +436,22 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, 
             // ---- O^T ---------------------------------------------------------------------------------
             uint32_t vw[4][NW], s01, s23;
             {
-                const int rows[4] = {vr0, vr1, vr0 + 8, vr1 + 8};
                 uint32_t sc[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int rw = rows[k];
+                for (int k = 0; k < 4; ++k) {   // rows vr0, vr1, vr0 + 8, vr1 + 8
+                    const int at = (k & 1 ? vw1 : vw0) + (k >> 1) * 8 * (D / 2);
                     if constexpr (D == 128) {
-                        const int pc = (g >> 1) ^ (((rw >> 1) & 1) << 1);
-                        const uint2 u = *reinterpret_cast<const uint2*>(stg + St::V + rw * 64 + pc * 16 + (g & 1) * 8);
+                        const uint2 u = *reinterpret_cast<const uint2*>(stg + at);
                         vw[k][0] = u.x; vw[k][1] = u.y;
-                        sc[k] = *reinterpret_cast<const uint8_t*>(stg + St::VS + rw * 4 + (g >> 1));
                     } else {
-                        vw[k][0] = *reinterpret_cast<const uint32_t*>(stg + St::V + rw * 32 + g * 4);
-                        sc[k] = *reinterpret_cast<const uint8_t*>(stg + St::VS + rw * 2 + (g >> 2));
+                        vw[k][0] = *reinterpret_cast<const uint32_t*>(stg + at);
                     }
-                    if (rw >= nv) sc[k] = 0;   // beyond the query: whatever the page holds counts as 0
+                    sc[k] = *reinterpret_cast<const uint8_t*>(stg + (k & 1 ? vs1 : vs0) + (k >> 1) * 8 * NG);
                 }
+                if (nv < kGran)   // beyond the query: whatever the page holds counts as 0
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if ((k & 1 ? vr1 : vr0) + (k >> 1) * 8 >= nv) sc[k] = 0;
                 s01 = e4m3x2_to_f16x2(sc[0] | sc[1] << 8);
                 s23 = e4m3x2_to_f16x2(sc[2] | sc[3] << 8);
             }
@@ -384,12 +466,18 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, 
                 uint32_t yl = __byte_perm(vw[2][w], vw[3][w], 0x5410), yh = __byte_perm(vw[2][w], vw[3][w], 0x7632);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint32_t mask = k & 1 ? 0x00f000f0u : 0x000f000fu;
-                    const __half2 mx = k & 1 ? tx : sx, ax = k & 1 ? hx : lx, my = k & 1 ? ty : sy, ay = k & 1 ? hy : ly;
-                    const uint32_t f[4] = {h2(__hfma2(h2((xl & mask) | 0x64006400u), mx, ax)),
-                                           h2(__hfma2(h2((xh & mask) | 0x64006400u), mx, ax)),
-                                           h2(__hfma2(h2((yl & mask) | 0x64006400u), my, ay)),
-                                           h2(__hfma2(h2((yh & mask) | 0x64006400u), my, ay))};
+                    uint32_t f[4];
+                    if (k & 1) {
+                        f[0] = h2(__hfma2(pick<0x00f000f0u>(xl, magic), tx, hx));
+                        f[1] = h2(__hfma2(pick<0x00f000f0u>(xh, magic), tx, hx));
+                        f[2] = h2(__hfma2(pick<0x00f000f0u>(yl, magic), ty, hy));
+                        f[3] = h2(__hfma2(pick<0x00f000f0u>(yh, magic), ty, hy));
+                    } else {
+                        f[0] = h2(__hfma2(pick<0x000f000fu>(xl, magic), sx, lx));
+                        f[1] = h2(__hfma2(pick<0x000f000fu>(xh, magic), sx, lx));
+                        f[2] = h2(__hfma2(pick<0x000f000fu>(yl, magic), sy, ly));
+                        f[3] = h2(__hfma2(pick<0x000f000fu>(yh, magic), sy, ly));
+                    }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][w * 4 + k], f, pb[nt][0], pb[nt][1]);
                     if (k == 1) { xl >>= 8; xh >>= 8; yl >>= 8; yh >>= 8; }
@@ -460,6 +548,10 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, 
                 *reinterpret_cast<float2*>(row + 2) = make_float2(t.z, t.w);
             }
         }
+        if (threadIdx.x == 0) {
+            if (s_lo == p0) a.span[x].x = blockIdx.x;
+            if (s_hi == p1) a.span[x].y = blockIdx.x;
+        }
         if (!whole && threadIdx.x < G) {
             pb[threadIdx.x * (D + 2) + D] = tot_m[threadIdx.x];
             pb[threadIdx.x * (D + 2) + D + 1] = tot_l[threadIdx.x];
@@ -478,25 +570,17 @@ __global__ void __launch_bounds__(D * kMergeY) q4_merge_kernel(Shape s, Attend a
     __shared__ float wt[kMaxBlocks], sums[kMaxBlocks], acc[kMergeY][D];
     __shared__ float red[32];
     pdl_wait();
-    const int x = blockIdx.x, G = s.g, BR = s.batch * s.hkv, col = threadIdx.x % D, y = threadIdx.x / D;
+    const int x = blockIdx.x, G = s.g, col = threadIdx.x % D, y = threadIdx.x / D;
+    const int2 sp = a.span[x];
+    const int c0 = sp.x, n = sp.y - sp.x + 1;
+    if (n == 1) return;   // finished in its block
     const int b = x / s.hkv, r = x % s.hkv;
-    const int p0 = a.pre[x], p1 = a.pre[x + 1], used = a.pre[BR + 1];
-    const long long total = a.pre[BR];
     __nv_bfloat16* out = a.O + ((long long)b * s.hq + r * G) * D;
-    if (p0 == p1) {
+    if (n == 0) {
         for (int h = blockIdx.y; h < G; h += gridDim.y)
             if (y == 0) out[h * D + col] = __float2bfloat16_rn(0.f);
         return;
     }
-    auto at = [&](int c) { return (int)(total * c / used); };
-    auto block_of = [&](int k) {   // the block whose range holds granule k
-        int c = (int)((long long)k * used / total);
-        while (c > 0 && at(c) > k) --c;
-        while (c + 1 < used && at(c + 1) <= k) ++c;
-        return c;
-    };
-    const int c0 = block_of(p0), c1 = block_of(p1 - 1), n = c1 - c0 + 1;
-    if (n == 1) return;   // finished in its block
     const long long stride = (long long)G * (D + 2);
     for (int h = blockIdx.y; h < G; h += gridDim.y) {
         // partial j: the last piece of block c0 (j = 0), the first piece of block c0 + j
@@ -543,7 +627,7 @@ template <int D, int NT>
 cudaError_t attend_t(const Shape& s, const Q4& c, const Routes& rt, const Attend& a, cudaStream_t st)
 {
     auto k = q4_attend_kernel<D, NT>;
-    const size_t smem = (size_t)Cfg<NT>::W * kStages * Stage<D>::BYTES;
+    const size_t smem = (size_t)Cfg<NT>::W * (kStages * Stage<D>::BYTES + sizeof(Meta));
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     e = launch_after(k, dim3(dec_tma_blocks()), dim3(32 * Cfg<NT>::W), smem, st, s, c, rt, a);
@@ -559,9 +643,9 @@ int q4_max_pairs() { return kMaxPairs; }
 size_t q4_part_floats(const Shape& s) { return (size_t)dec_tma_blocks() * 2 * s.g * (s.d + 2); }
 
 cudaError_t launch_attend_q4(const Shape& s, const Q4& c, const void* q, const int* seqlens, const Routes& rt, bool dense,
-                             float* part, int* pre, void* O, cudaStream_t st)
+                             float* part, int* span, void* O, cudaStream_t st)
 {
-    const Attend a{(const __nv_bfloat16*)q, seqlens, dense ? 1 : 0, part, pre, (__nv_bfloat16*)O};
+    const Attend a{(const __nv_bfloat16*)q, seqlens, dense ? 1 : 0, part, reinterpret_cast<int2*>(span), (__nv_bfloat16*)O};
     if (s.d == 128) return s.g <= 8 ? attend_t<128, 1>(s, c, rt, a, st) : attend_t<128, 2>(s, c, rt, a, st);
     return s.g <= 8 ? attend_t<64, 1>(s, c, rt, a, st) : attend_t<64, 2>(s, c, rt, a, st);
 }

@@ -62,11 +62,13 @@ def attend(q, k, v, bias, k_scale):
     p = np.exp(z - zm)
     l = p.sum(1, keepdims=True)
     o = p @ v / l
-    # logits: per scale group the operand 128 + u starts from -136 sum(q): fp32 sums of 32 terms of size
-    # up to 143 |q| and of 136 |sum(q)|, a handful of roundings (2^-23 of the running sum each, truncated)
+    # logits, per scale group of the key (its scale s times codes u - 8): fp32 sums of 32 products with codes up to
+    # 15, and 8 sum(q) taken off: |terms| below 23 sum|q|, a handful (8) of truncations of 2^-23 each; the query is
+    # exact to 2^-27 of its largest element, sum(q) to 2^-22
     on = np.isfinite(bias)
     qs = np.abs(q).reshape(len(q), -1, 32).sum(2)                       # [g, groups]
-    dz = 2.0 ** -20 * 136 * (qs @ k_scale[on].T).max(1) / np.sqrt(d)    # [g]
+    unit = 2.0 ** -20 * 23 * qs + 2.0 ** -27 * 7 * 32 * np.abs(q).max(1, keepdims=True)
+    dz = (unit @ k_scale[on].T).max(1) / np.sqrt(d)                     # [g]
     dz = dz + 2.0 ** -20 * (np.abs(zm[:, 0]) + np.abs(z[:, on] - zm).max(1))   # scaling, bias, exp2 argument
     # weights: 2^-11 relative for f16 (2^-25 absolute below its normals, against weights of at least 1/64 at the
     # maximum), the error of the exponent, fp32 sums of n terms
