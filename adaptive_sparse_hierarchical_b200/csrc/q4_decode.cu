@@ -5,13 +5,13 @@
 // over the routed chunks (bias of the chunk) and the query's own chunk (bias 0); gamma = 0 takes
 // every chunk with bias 0.
 //
-// Work is cut into granules of 16 tokens.  The granules of all (sequence, KV head) pairs form one
+// Work is cut into granules of 32 tokens (16 for chunks of 16).  The granules of all (sequence, KV head) pairs form one
 // list that the blocks share evenly; a block's warps take its granules in turn, each with its own
 // online softmax and its own ring of cp.async stages (a granule is used by one warp only, so no
 // barrier is involved), and merge at the end of a pair.  A pair inside one block is finished there;
 // pieces of a pair that spans blocks are merged by a second kernel, in block order.
 //
-// A warp computes S^T = K q^T and O^T = V^T P^T: the 16 tokens (then 16 of the d_h elements) are the
+// A warp computes S^T = K q^T and O^T = V^T P^T: 16 tokens (then 16 of the d_h elements) are the
 // 16 rows of m16n8k16 MMAs and the heads the 8 columns, so groups of up to 8 heads fill the tile.
 //   K: the f16 number with the bits of a code u in its lowest bits is u 2^-24, in the next four 16 u
 //      2^-24 (subnormals: linear, and exact in the MMA): two masks, a shift and two masks turn a word
@@ -31,14 +31,14 @@
 // f16 pipes that unpack the codes.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "q4.cuh"
 #include "stage2_mma.cuh"
 
 namespace dash {
 namespace {
 
-constexpr int kGran = 16;         // tokens per granule
-constexpr int kStages = 4;
 constexpr int kMaxPairs = 2048;
 constexpr int kMeta = 64;         // granule descriptors per warp (two halves of 32)
 
@@ -52,9 +52,12 @@ struct Meta {
 // Warps per block: one block per SM, as many warps as the registers of NT head tiles allow.
 template <int NT> struct Cfg { static constexpr int W = NT == 1 ? 16 : 12; };
 
-template <int D>
+// Granules of 16 U tokens (U = 2 wherever the chunk allows: descriptors, waits and votes are paid once for
+// twice the tokens, and the warp has two independent chains to issue from); the ring holds 64 tokens.
+template <int D, int U>
 struct Stage {
-    static constexpr int CODES = kGran * D / 2, SCALES = kGran * D / kGrp;
+    static constexpr int GRAN = 16 * U, N = 4 / U;
+    static constexpr int CODES = GRAN * D / 2, SCALES = GRAN * D / kGrp;
     static constexpr int K = 0, V = CODES, KS = 2 * CODES, VS = 2 * CODES + SCALES, BYTES = 2 * (CODES + SCALES);
     static constexpr int OLD = D + 4;   // row length of the merge buffer [8 NT][OLD] that reuses a warp's ring
 };
@@ -110,7 +113,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-// Token (row of the granule) behind row m < 8 of S^T (row m + 8: the same + 8).  Even rows 0..3 and
+// Token (row of 16 tokens) behind row m < 8 of S^T (row m + 8: the same + 8).  Even rows 0..3 and
 // odd rows 5, 4, 7, 6: keys read two rows of opposite parity at once, values rows 0..3 or 4..7,
 // which the swizzle of the value rows spreads over all banks.
 __device__ __forceinline__ int tok_of(int m) { return (m & 1) ? ((m >> 1) ^ 1) + 4 : m >> 1; }
@@ -118,11 +121,12 @@ __device__ __forceinline__ int tok_of(int m) { return (m & 1) ? ((m >> 1) ^ 1) +
 // Length of sequence b as the kernels use it, granules of a pair.
 __device__ __forceinline__ int len_of(const Shape& s, const int* seqlens, int b) { return min(max(seqlens[b], 0), s.n); }
 
-template <int D, int NT>
+template <int D, int NT, int U>
 __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, Q4 c, Routes rt, Attend a)
 {
-    constexpr int W = Cfg<NT>::W, NG = D / kGrp, NW = D / 64, MT = D / 16, OLD = Stage<D>::OLD;
-    using St = Stage<D>;
+    constexpr int W = Cfg<NT>::W, NG = D / kGrp, NW = D / 64, MT = D / 16;
+    using St = Stage<D, U>;
+    constexpr int OLD = St::OLD, kGran = St::GRAN, kStages = St::N;
     static_assert(8 * NT * OLD * 4 <= kStages * St::BYTES, "the merge buffer reuses a warp's ring");
     extern __shared__ __align__(128) char smem[];
     __shared__ int pre[kMaxPairs + 1];
@@ -243,22 +247,25 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, 
                 const unsigned long long sc = reinterpret_cast<const unsigned long long*>(&meta.sc[k])[(lane / SP) & 1];
                 // 16-byte pieces 0, 1 and 2, 3 of a value row change places in rows 2, 3, 6, 7, ...; the value
                 // scales follow the key scales in the stage; zeros where the page is not mapped
-                if constexpr (D == 128)
-                    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.lt.s32 p, %5, 256;\n\tsetp.ne.s32 q, %7, 0;\n\t"
-                                 "cp.async.cg.shared.global [%0], [%2], 16, p;\n\t"
-                                 "cp.async.cg.shared.global [%0 + 512], [%2 + 512], 16, p;\n\t"
-                                 "cp.async.cg.shared.global [%1 + 1024], [%3], 16, p;\n\t"
-                                 "cp.async.cg.shared.global [%1 + 1536], [%3 + 512], 16, p;\n\t"
-                                 "@q cp.async.cg.shared.global [%0 + %6], [%4], 16, p;\n\t}\n" ::"r"(dst + lane16),
-                                 "r"(dst + vlane16), "l"(kv.x + lane16), "l"(kv.y + lane16),
-                                 "l"(sc + lane16 % (SP * 16)), "r"(meta.nv[k]), "n"(St::KS), "r"((int)(lane < 2 * SP)));
-                else
-                    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.lt.s32 p, %5, 256;\n\tsetp.ne.s32 q, %7, 0;\n\t"
-                                 "cp.async.cg.shared.global [%0], [%2], 16, p;\n\t"
-                                 "cp.async.cg.shared.global [%1 + 512], [%3], 16, p;\n\t"
-                                 "@q cp.async.cg.shared.global [%0 + %6], [%4], 16, p;\n\t}\n" ::"r"(dst + lane16),
-                                 "r"(dst + vlane16), "l"(kv.x + lane16), "l"(kv.y + lane16),
-                                 "l"(sc + lane16 % (SP * 16)), "r"(meta.nv[k]), "n"(St::KS), "r"((int)(lane < 2 * SP)));
+                asm volatile("{\n\t.reg .pred p, q;\n\tsetp.lt.s32 p, %5, 256;\n\tsetp.ne.s32 q, %7, 0;\n\t"
+                             "cp.async.cg.shared.global [%0], [%2], 16, p;\n\t"
+                             "cp.async.cg.shared.global [%1 + %8], [%3], 16, p;\n\t"
+                             "@q cp.async.cg.shared.global [%0 + %6], [%4], 16, p;\n\t}\n" ::"r"(dst + lane16),
+                             "r"(dst + vlane16), "l"(kv.x + lane16), "l"(kv.y + lane16),
+                             "l"(sc + lane16 % (SP * 16)), "r"(meta.nv[k]), "n"(St::KS), "r"((int)(lane < 2 * SP)),
+                             "n"(St::V));
+                auto more = [&](auto off) {   // the pieces from 512 bytes on
+                    asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.s32 p, %4, 256;\n\t"
+                                 "cp.async.cg.shared.global [%0 + %5], [%2 + %5], 16, p;\n\t"
+                                 "cp.async.cg.shared.global [%1 + %6], [%3 + %5], 16, p;\n\t}\n" ::"r"(dst + lane16),
+                                 "r"(dst + vlane16), "l"(kv.x + lane16), "l"(kv.y + lane16), "r"(meta.nv[k]),
+                                 "n"(decltype(off)::value), "n"(St::V + decltype(off)::value));
+                };
+                if constexpr (St::CODES >= 1024) more(std::integral_constant<int, 512>());
+                if constexpr (St::CODES >= 2048) {
+                    more(std::integral_constant<int, 1024>());
+                    more(std::integral_constant<int, 1536>());
+                }
             }
             cp_async_commit();
         };
@@ -327,8 +334,10 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, 
             for (int m = 0; m < MT; ++m) o[nt][m][0] = o[nt][m][1] = o[nt][m][2] = o[nt][m][3] = 0.f;
         }
 
+        // The last granule of a pair may end before its last token: FULL = false.
         uint32_t cur = 0, nxt = (kStages - 1) * St::BYTES;   // ring offsets of granule m and of the one to load
-        for (int m = 0; m < nm; ++m) {
+        auto step = [&](int m, auto full_c) {
+            constexpr bool FULL = decltype(full_c)::value;
             if ((m & 31) == 0) fetch(m + 32);
             if ((m & 31) == 16) publish(m + 16);
             cp_async_wait<kStages - 2>();
@@ -337,153 +346,170 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, 
             const char* stg = ring + cur;
             nxt = cur;
             cur = cur == (kStages - 1) * St::BYTES ? 0 : cur + St::BYTES;
-            const int nv = meta.nv[m & (kMeta - 1)] & 255;
+            const int nv = FULL ? kGran : meta.nv[m & (kMeta - 1)] & 255;
             const float bias2 = meta.bias[m & (kMeta - 1)];
 
-            // ---- S^T ---------------------------------------------------------------------------------
-            uint32_t ka[NG], kb[NG], sa, sb;
-            if constexpr (D == 128) {
-                const uint4 u = *reinterpret_cast<const uint4*>(stg + St::K + tk * 64 + t4 * 16);
-                const uint4 v = *reinterpret_cast<const uint4*>(stg + St::K + (tk + 8) * 64 + t4 * 16);
-                ka[0] = u.x; ka[1] = u.y; ka[2] = u.z; ka[3] = u.w;
-                kb[0] = v.x; kb[1] = v.y; kb[2] = v.z; kb[3] = v.w;
-                sa = *reinterpret_cast<const uint32_t*>(stg + St::KS + tk * 4);
-                sb = *reinterpret_cast<const uint32_t*>(stg + St::KS + (tk + 8) * 4);
-            } else {
-                const uint2 u = *reinterpret_cast<const uint2*>(stg + St::K + tk * 32 + t4 * 8);
-                const uint2 v = *reinterpret_cast<const uint2*>(stg + St::K + (tk + 8) * 32 + t4 * 8);
-                ka[0] = u.x; ka[1] = u.y;
-                kb[0] = v.x; kb[1] = v.y;
-                sa = *reinterpret_cast<const uint16_t*>(stg + St::KS + tk * 2);
-                sb = *reinterpret_cast<const uint16_t*>(stg + St::KS + (tk + 8) * 2);
-            }
-            uint32_t fa[NG / 2], fb[NG / 2];   // scales of this lane's two tokens, f16x2
+            // ---- S^T: rows 16 u + (tok_of(g), + 8), columns heads 2 t4, 2 t4 + 1 -------------------------
+            float z[U][NT][4];
 #pragma unroll
-            for (int k = 0; k < NG / 2; ++k) {
-                fa[k] = e4m3x2_to_f16x2(sa >> (16 * k));
-                fb[k] = e4m3x2_to_f16x2(sb >> (16 * k));
-            }
-            float z[NT][4];
-            {
-                const uint32_t ua = (t4 & 1) ? fa[NG / 2 - 1] : fa[0], ub = (t4 & 1) ? fb[NG / 2 - 1] : fb[0];
-                const __half2 e8 = __float2half2_rn(0.00390625f);   // 2^-8: with the sums' 2^-13, 8 times the codes' 2^-24
-                const uint32_t f[4] = {h2(__hmul2(h2(ua), e8)), h2(__hmul2(h2(ub), e8)), 0u, 0u};
+            for (int u = 0; u < U; ++u) {
+                const char* ks = stg + St::K + u * 8 * D;
+                const char* sc = stg + St::KS + u * 16 * NG;
+                uint32_t ka[NG], kb[NG], sa, sb;
+                if constexpr (D == 128) {
+                    const uint4 x4 = *reinterpret_cast<const uint4*>(ks + tk * 64 + t4 * 16);
+                    const uint4 y4 = *reinterpret_cast<const uint4*>(ks + (tk + 8) * 64 + t4 * 16);
+                    ka[0] = x4.x; ka[1] = x4.y; ka[2] = x4.z; ka[3] = x4.w;
+                    kb[0] = y4.x; kb[1] = y4.y; kb[2] = y4.z; kb[3] = y4.w;
+                    sa = *reinterpret_cast<const uint32_t*>(sc + tk * 4);
+                    sb = *reinterpret_cast<const uint32_t*>(sc + (tk + 8) * 4);
+                } else {
+                    const uint2 x2 = *reinterpret_cast<const uint2*>(ks + tk * 32 + t4 * 8);
+                    const uint2 y2 = *reinterpret_cast<const uint2*>(ks + (tk + 8) * 32 + t4 * 8);
+                    ka[0] = x2.x; ka[1] = x2.y;
+                    kb[0] = y2.x; kb[1] = y2.y;
+                    sa = *reinterpret_cast<const uint16_t*>(sc + tk * 2);
+                    sb = *reinterpret_cast<const uint16_t*>(sc + (tk + 8) * 2);
+                }
+                uint32_t fa[NG / 2], fb[NG / 2];   // scales of this lane's two tokens, f16x2
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_f16_0(z[nt], f, qs[nt], 0u);
-            }
+                for (int k = 0; k < NG / 2; ++k) {
+                    fa[k] = e4m3x2_to_f16x2(sa >> (16 * k));
+                    fb[k] = e4m3x2_to_f16x2(sb >> (16 * k));
+                }
+                {
+                    const uint32_t ua = (t4 & 1) ? fa[NG / 2 - 1] : fa[0], ub = (t4 & 1) ? fb[NG / 2 - 1] : fb[0];
+                    const __half2 e8 = __float2half2_rn(0.00390625f);   // 2^-8: with the sums' 2^-13, 8 times 2^-24
+                    const uint32_t f[4] = {h2(__hmul2(h2(ua), e8)), h2(__hmul2(h2(ub), e8)), 0u, 0u};
 #pragma unroll
-            for (int gg = 0; gg < NG; ++gg) {
-                const uint32_t w = ka[gg], v = kb[gg], w8 = w >> 8, v8 = v >> 8;
-                const uint32_t f0[4] = {w & 0x000f000fu, v & 0x000f000fu, w & 0x00f000f0u, v & 0x00f000f0u};
-                const uint32_t f1[4] = {w8 & 0x000f000fu, v8 & 0x000f000fu, w8 & 0x00f000f0u, v8 & 0x00f000f0u};
-                const float2 pa = __half22float2(h2(fa[gg / 2])), pc = __half22float2(h2(fb[gg / 2]));
-                const float xa = gg & 1 ? pa.y : pa.x, xb = gg & 1 ? pc.y : pc.x;
+                    for (int nt = 0; nt < NT; ++nt) mma_f16_0(z[u][nt], f, qs[nt], 0u);
+                }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float d[4];
-                    mma_f16_0(d, f0, qf[nt][gg][0], qf[nt][gg][1]);
-                    mma_f16(d, f1, qf[nt][gg][2], qf[nt][gg][3]);
-                    z[nt][0] = fmaf(xa, d[0], z[nt][0]);
-                    z[nt][1] = fmaf(xa, d[1], z[nt][1]);
-                    z[nt][2] = fmaf(xb, d[2], z[nt][2]);
-                    z[nt][3] = fmaf(xb, d[3], z[nt][3]);
+                for (int gg = 0; gg < NG; ++gg) {
+                    const uint32_t w = ka[gg], v = kb[gg], w8 = w >> 8, v8 = v >> 8;
+                    const uint32_t f0[4] = {w & 0x000f000fu, v & 0x000f000fu, w & 0x00f000f0u, v & 0x00f000f0u};
+                    const uint32_t f1[4] = {w8 & 0x000f000fu, v8 & 0x000f000fu, w8 & 0x00f000f0u, v8 & 0x00f000f0u};
+                    const float2 pa = __half22float2(h2(fa[gg / 2])), pc = __half22float2(h2(fb[gg / 2]));
+                    const float xa = gg & 1 ? pa.y : pa.x, xb = gg & 1 ? pc.y : pc.x;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float d[4];
+                        mma_f16_0(d, f0, qf[nt][gg][0], qf[nt][gg][1]);
+                        mma_f16(d, f1, qf[nt][gg][2], qf[nt][gg][3]);
+                        z[u][nt][0] = fmaf(xa, d[0], z[u][nt][0]);
+                        z[u][nt][1] = fmaf(xa, d[1], z[u][nt][1]);
+                        z[u][nt][2] = fmaf(xb, d[2], z[u][nt][2]);
+                        z[u][nt][3] = fmaf(xb, d[3], z[u][nt][3]);
+                    }
                 }
             }
             // logits relative to the reference; before the first one it is -inf and they are +inf
-            float tz[NT][4], most = -INFINITY;
+            float most = -INFINITY, tz[U][NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+                const float c0 = bias2 - ref[nt][0], c1 = bias2 - ref[nt][1];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) tz[nt][e] = fmaf(z[nt][e], fac[nt][e & 1], bias2 - ref[nt][e & 1]);
-                if (nv < kGran) {   // the end of the query's own chunk
-                    if (tk >= nv) tz[nt][0] = tz[nt][1] = -INFINITY;
-                    if (tk + 8 >= nv) tz[nt][2] = tz[nt][3] = -INFINITY;
+                for (int u = 0; u < U; ++u) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) tz[u][nt][e] = fmaf(z[u][nt][e], fac[nt][e & 1], e & 1 ? c1 : c0);
+                    if (!FULL) {
+                        if (16 * u + tk >= nv) tz[u][nt][0] = tz[u][nt][1] = -INFINITY;
+                        if (16 * u + tk + 8 >= nv) tz[u][nt][2] = tz[u][nt][3] = -INFINITY;
+                    }
+                    most = fmaxf(most, fmaxf(fmaxf(tz[u][nt][0], tz[u][nt][1]), fmaxf(tz[u][nt][2], tz[u][nt][3])));
                 }
-                most = fmaxf(most, fmaxf(fmaxf(tz[nt][0], tz[nt][1]), fmaxf(tz[nt][2], tz[nt][3])));
             }
             if (__any_sync(0xffffffffu, most > 6.f)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float y0 = fmaf(z[nt][e], fac[nt][e], bias2), y1 = fmaf(z[nt][e + 2], fac[nt][e], bias2);
-                        if (tk >= nv) y0 = -INFINITY;
-                        if (tk + 8 >= nv) y1 = -INFINITY;
-                        float mx = fmaxf(y0, y1);
+                        float mx = ref[nt][e];
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            float y0 = fmaf(z[u][nt][e], fac[nt][e], bias2), y1 = fmaf(z[u][nt][e + 2], fac[nt][e], bias2);
+                            if (!FULL && 16 * u + tk >= nv) y0 = -INFINITY;
+                            if (!FULL && 16 * u + tk + 8 >= nv) y1 = -INFINITY;
+                            tz[u][nt][e] = y0;
+                            tz[u][nt][e + 2] = y1;
+                            mx = fmaxf(mx, fmaxf(y0, y1));
+                        }
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        mx = fmaxf(mx, ref[nt][e]);
                         const float base = mx == -INFINITY ? 0.f : mx, cr = exp2f(ref[nt][e] - base);
                         ref[nt][e] = mx;
-                        tz[nt][e] = y0 - base;
-                        tz[nt][e + 2] = y1 - base;
                         l[nt][e] *= cr;
+#pragma unroll
+                        for (int u = 0; u < U; ++u) { tz[u][nt][e] -= base; tz[u][nt][e + 2] -= base; }
 #pragma unroll
                         for (int k = 0; k < MT; ++k) { o[nt][k][e] *= cr; o[nt][k][e + 2] *= cr; }
                     }
             }
-            uint32_t pb[NT][2];
+            uint32_t pb[U][NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float q0 = ex2(tz[nt][0]), q1 = ex2(tz[nt][1]), q2 = ex2(tz[nt][2]), q3 = ex2(tz[nt][3]);
-                l[nt][0] += q0 + q2;
-                l[nt][1] += q1 + q3;
-                pb[nt][0] = movm_t(pack_f16(q0, q1));
-                pb[nt][1] = movm_t(pack_f16(q2, q3));
-            }
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float q0 = ex2(tz[u][nt][0]), q1 = ex2(tz[u][nt][1]), q2 = ex2(tz[u][nt][2]), q3 = ex2(tz[u][nt][3]);
+                    l[nt][0] += q0 + q2;
+                    l[nt][1] += q1 + q3;
+                    pb[u][nt][0] = movm_t(pack_f16(q0, q1));
+                    pb[u][nt][1] = movm_t(pack_f16(q2, q3));
+                }
 
-            // ---- O^T ---------------------------------------------------------------------------------
-            uint32_t vw[4][NW], s01, s23;
-            {
-                uint32_t sc[4];
+            // ---- O^T -----------------------------------------------------------------------------------
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                uint32_t vw[4][NW], sc[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {   // rows vr0, vr1, vr0 + 8, vr1 + 8
-                    const int at = (k & 1 ? vw1 : vw0) + (k >> 1) * 8 * (D / 2);
+                    const int at = (k & 1 ? vw1 : vw0) + (16 * u + (k >> 1) * 8) * (D / 2);
                     if constexpr (D == 128) {
-                        const uint2 u = *reinterpret_cast<const uint2*>(stg + at);
-                        vw[k][0] = u.x; vw[k][1] = u.y;
+                        const uint2 x2 = *reinterpret_cast<const uint2*>(stg + at);
+                        vw[k][0] = x2.x; vw[k][1] = x2.y;
                     } else {
                         vw[k][0] = *reinterpret_cast<const uint32_t*>(stg + at);
                     }
-                    sc[k] = *reinterpret_cast<const uint8_t*>(stg + (k & 1 ? vs1 : vs0) + (k >> 1) * 8 * NG);
+                    sc[k] = *reinterpret_cast<const uint8_t*>(stg + (k & 1 ? vs1 : vs0) + (16 * u + (k >> 1) * 8) * NG);
+                    // beyond the query: whatever the page holds counts as 0
+                    if (!FULL && 16 * u + (k & 1 ? vr1 : vr0) + (k >> 1) * 8 >= nv) sc[k] = 0;
                 }
-                if (nv < kGran)   // beyond the query: whatever the page holds counts as 0
+                const uint32_t s01 = e4m3x2_to_f16x2(sc[0] | sc[1] << 8), s23 = e4m3x2_to_f16x2(sc[2] | sc[3] << 8);
+                // multipliers and offsets of the two code positions, for rows (vr0, vr1) and (+8)
+                const __half2 sx = __hmul2(h2(s01), __float2half2_rn(0.0625f)), sy = __hmul2(h2(s23), __float2half2_rn(0.0625f));
+                const __half2 lx = __hmul2(sx, __float2half2_rn(-1032.f)), ly = __hmul2(sy, __float2half2_rn(-1032.f));
+                const __half2 hx = __hmul2(sx, __float2half2_rn(-72.f)), hy = __hmul2(sy, __float2half2_rn(-72.f));
+                const __half2 tx = __hmul2(sx, __float2half2_rn(0.0625f)), ty = __hmul2(sy, __float2half2_rn(0.0625f));
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if ((k & 1 ? vr1 : vr0) + (k >> 1) * 8 >= nv) sc[k] = 0;
-                s01 = e4m3x2_to_f16x2(sc[0] | sc[1] << 8);
-                s23 = e4m3x2_to_f16x2(sc[2] | sc[3] << 8);
-            }
-            // multipliers and offsets of the two code positions, for rows (vr0, vr1) and (+8)
-            const __half2 sx = __hmul2(h2(s01), __float2half2_rn(0.0625f)), sy = __hmul2(h2(s23), __float2half2_rn(0.0625f));
-            const __half2 lx = __hmul2(sx, __float2half2_rn(-1032.f)), ly = __hmul2(sy, __float2half2_rn(-1032.f));
-            const __half2 hx = __hmul2(sx, __float2half2_rn(-72.f)), hy = __hmul2(sy, __float2half2_rn(-72.f));
-            const __half2 tx = __hmul2(sx, __float2half2_rn(0.0625f)), ty = __hmul2(sy, __float2half2_rn(0.0625f));
+                for (int w = 0; w < NW; ++w) {
+                    uint32_t xl = __byte_perm(vw[0][w], vw[1][w], 0x5410), xh = __byte_perm(vw[0][w], vw[1][w], 0x7632);
+                    uint32_t yl = __byte_perm(vw[2][w], vw[3][w], 0x5410), yh = __byte_perm(vw[2][w], vw[3][w], 0x7632);
 #pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                uint32_t xl = __byte_perm(vw[0][w], vw[1][w], 0x5410), xh = __byte_perm(vw[0][w], vw[1][w], 0x7632);
-                uint32_t yl = __byte_perm(vw[2][w], vw[3][w], 0x5410), yh = __byte_perm(vw[2][w], vw[3][w], 0x7632);
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t f[4];
+                        if (k & 1) {
+                            f[0] = h2(__hfma2(pick<0x00f000f0u>(xl, magic), tx, hx));
+                            f[1] = h2(__hfma2(pick<0x00f000f0u>(xh, magic), tx, hx));
+                            f[2] = h2(__hfma2(pick<0x00f000f0u>(yl, magic), ty, hy));
+                            f[3] = h2(__hfma2(pick<0x00f000f0u>(yh, magic), ty, hy));
+                        } else {
+                            f[0] = h2(__hfma2(pick<0x000f000fu>(xl, magic), sx, lx));
+                            f[1] = h2(__hfma2(pick<0x000f000fu>(xh, magic), sx, lx));
+                            f[2] = h2(__hfma2(pick<0x000f000fu>(yl, magic), sy, ly));
+                            f[3] = h2(__hfma2(pick<0x000f000fu>(yh, magic), sy, ly));
+                        }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t f[4];
-                    if (k & 1) {
-                        f[0] = h2(__hfma2(pick<0x00f000f0u>(xl, magic), tx, hx));
-                        f[1] = h2(__hfma2(pick<0x00f000f0u>(xh, magic), tx, hx));
-                        f[2] = h2(__hfma2(pick<0x00f000f0u>(yl, magic), ty, hy));
-                        f[3] = h2(__hfma2(pick<0x00f000f0u>(yh, magic), ty, hy));
-                    } else {
-                        f[0] = h2(__hfma2(pick<0x000f000fu>(xl, magic), sx, lx));
-                        f[1] = h2(__hfma2(pick<0x000f000fu>(xh, magic), sx, lx));
-                        f[2] = h2(__hfma2(pick<0x000f000fu>(yl, magic), sy, ly));
-                        f[3] = h2(__hfma2(pick<0x000f000fu>(yh, magic), sy, ly));
+                        for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][w * 4 + k], f, pb[u][nt][0], pb[u][nt][1]);
+                        if (k == 1) { xl >>= 8; xh >>= 8; yl >>= 8; yh >>= 8; }
                     }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][w * 4 + k], f, pb[nt][0], pb[nt][1]);
-                    if (k == 1) { xl >>= 8; xh >>= 8; yl >>= 8; yh >>= 8; }
                 }
             }
-        }
+        };
+        // the pair's last granule, where it is partly filled, is this warp's last one or another warp's
+        const bool part = nm > 0 && s_lo - p0 + warp + (nm - 1) * W == p1 - p0 - 1 && (i + 1) % kGran != 0;
+        for (int m = 0; m < nm - part; ++m) step(m, std::true_type());
+        if (part) step(nm - 1, std::false_type());
 
         // ---- merge the warps (fixed order), each through its own drained ring -----------------------
         cp_async_wait<0>();
@@ -623,17 +649,24 @@ __global__ void __launch_bounds__(D * kMergeY) q4_merge_kernel(Shape s, Attend a
     }
 }
 
-template <int D, int NT>
+template <int D, int NT, int U>
 cudaError_t attend_t(const Shape& s, const Q4& c, const Routes& rt, const Attend& a, cudaStream_t st)
 {
-    auto k = q4_attend_kernel<D, NT>;
-    const size_t smem = (size_t)Cfg<NT>::W * (kStages * Stage<D>::BYTES + sizeof(Meta));
+    auto k = q4_attend_kernel<D, NT, U>;
+    const size_t smem = (size_t)Cfg<NT>::W * (Stage<D, U>::N * Stage<D, U>::BYTES + sizeof(Meta));
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     e = launch_after(k, dim3(dec_tma_blocks()), dim3(32 * Cfg<NT>::W), smem, st, s, c, rt, a);
     if (e != cudaSuccess) return e;
     const int pairs = s.batch * s.hkv;
     return launch_after(q4_merge_kernel<D>, dim3(pairs, pairs * s.g <= 1024 ? s.g : 1), dim3(D * kMergeY), 0, st, s, a, c.vexp);
+}
+
+template <int D>
+cudaError_t attend_d(const Shape& s, const Q4& c, const Routes& rt, const Attend& a, cudaStream_t st)
+{
+    if (s.B % 32 == 0) return s.g <= 8 ? attend_t<D, 1, 2>(s, c, rt, a, st) : attend_t<D, 2, 2>(s, c, rt, a, st);
+    return s.g <= 8 ? attend_t<D, 1, 1>(s, c, rt, a, st) : attend_t<D, 2, 1>(s, c, rt, a, st);
 }
 
 }  // namespace
@@ -646,8 +679,7 @@ cudaError_t launch_attend_q4(const Shape& s, const Q4& c, const void* q, const i
                              float* part, int* span, void* O, cudaStream_t st)
 {
     const Attend a{(const __nv_bfloat16*)q, seqlens, dense ? 1 : 0, part, reinterpret_cast<int2*>(span), (__nv_bfloat16*)O};
-    if (s.d == 128) return s.g <= 8 ? attend_t<128, 1>(s, c, rt, a, st) : attend_t<128, 2>(s, c, rt, a, st);
-    return s.g <= 8 ? attend_t<64, 1>(s, c, rt, a, st) : attend_t<64, 2>(s, c, rt, a, st);
+    return s.d == 128 ? attend_d<128>(s, c, rt, a, st) : attend_d<64>(s, c, rt, a, st);
 }
 
 }  // namespace dash
