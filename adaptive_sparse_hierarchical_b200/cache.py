@@ -3,24 +3,29 @@
 kernels of libdash_b200.so."""
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import _lib as L
 from .api import _st
 
-_CONTEXT = contextlib.nullcontext()
+def _current(index):
+    """Raw handle of device `index`'s current stream."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _within(device, stream):
     """Context in which `device` is current and allocations and copies go to `stream` (None: the
     device's current stream)."""
     if stream is None:
-        return _CONTEXT if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        return torch.cuda.device(device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
     return torch.cuda.stream(stream)
+
+
+def _elsewhere(index, stream):
+    """Whether a call must first make another device or stream current."""
+    return stream is not None or torch._C._cuda_getDevice() != index
 
 
 def _need(t, name, device, dtype, shape=None):
@@ -29,6 +34,11 @@ def _need(t, name, device, dtype, shape=None):
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(shape)} is needed, not {tuple(t.shape)}")
     return t
+
+
+def _signature(t):
+    """What the checks of an argument depend on."""
+    return (t.shape, t.stride(), t.dtype, t.device) if isinstance(t, torch.Tensor) else type(t)
 
 
 class Q4DecodeState:
@@ -51,6 +61,8 @@ class Q4DecodeState:
             num_pages = batch * slots
         self.page_table = page_table.to(device=device, dtype=torch.int32).contiguous()
         self.device = self.page_table.device
+        self._index = self.device.index
+        self._lib = L.load()
         self.page_size = page_size
         new = dict(dtype=torch.uint8, device=self.device)
         self.k_codes = torch.zeros((num_pages, h_kv, page_size, d // 2), **new)
@@ -67,77 +79,104 @@ class Q4DecodeState:
         self._shape = dict(batch=batch, seqlen=capacity, h_q=h_q, h_kv=h_kv, d_h=d, chunk=chunk, alpha=alpha,
                            gamma=gamma, inv_sigma=inv_sigma, dtype=L.DASH_BF16)
         self.p = L.params(**self._shape)
-        self._strided = {}
+        self._seen = {}   # arguments that passed the checks, by signature: their parameters
         self.kv = L.q4_kv(self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.page_table,
                           page_size=page_size, k_exp=k_exp, v_exp=v_exp)
         ws = L.dash_q4_workspace_size(self.p)
         self.workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=self.device)
+        self._ws_bytes = self.workspace.shape[0]
         self.route = None
 
     def _tokens(self, t, name):
         """t as [batch, n, h_kv, d] with contiguous d."""
         s = self._shape
-        if t.dim() == 3:
+        if isinstance(t, torch.Tensor) and t.dim() == 3:
             t = t.unsqueeze(1)
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise TypeError(f"{name}: a tensor [batch, tokens, h_kv, d] is needed")
         _need(t, name, self.device, torch.bfloat16, (s["batch"], t.shape[1], s["h_kv"], s["d_h"]))
         if t.stride(3) != 1:
             raise ValueError(f"{name}: the head dimension must be contiguous")
         return t
 
-    def _params(self, k, v):
-        key = (k.stride(), v.stride())
-        p = self._strided.get(key)
-        if p is None:
-            if len(self._strided) > 64:
-                self._strided.clear()
-            p = self._strided[key] = L.params(**self._shape, k_strides=_st(k), v_strides=_st(v))
-        return p
+    def _check(self, what, k, v, rows, name):
+        """dash_params and token number for K/V arguments k, v and an int32 [batch] argument (or None)."""
+        key = (what, _signature(k), _signature(v), _signature(rows))
+        got = self._seen.get(key)
+        if got is None:
+            s = self._shape
+            k4, v4 = self._tokens(k, "K"), self._tokens(v, "V")
+            if k4.shape[1] != v4.shape[1]:
+                raise ValueError("K and V hold different numbers of tokens")
+            if rows is not None and not _need(rows, name, self.device, torch.int32, (s["batch"],)).is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            if len(self._seen) > 64:
+                self._seen.clear()
+            got = self._seen[key] = L.params(**s, k_strides=_st(k4), v_strides=_st(v4)), k4.shape[1]
+        return got
 
     def append(self, k_new, v_new, counts=None, stream=None):
         """Append k_new, v_new [batch, n, h_kv, d] (or [batch, h_kv, d]: one token): the first
         counts[b] (device int32; None: all n) tokens of each sequence, in 4 bits, and their summaries."""
-        k, v = self._tokens(k_new, "k_new"), self._tokens(v_new, "v_new")
-        if k.shape[1] != v.shape[1]:
-            raise ValueError("k_new and v_new hold different numbers of tokens")
-        if counts is not None and not _need(counts, "counts", self.device, torch.int32, self.seqlens.shape).is_contiguous():
-            raise ValueError("counts must be contiguous")
-        _need(self.qbar, "qbar", self.device, torch.float32, (self._shape["h_kv"], self._shape["d_h"]))
-        with _within(self.device, stream):
-            L.dash_append_q4(self._params(k, v), self.kv, k, v, k.shape[1], counts, self.qbar, self.kbar, self.state,
-                             self.seqlens)
+        if _elsewhere(self._index, stream):
+            with _within(self.device, stream):
+                return self.append(k_new, v_new, counts)
+        p, n = self._check("append", k_new, v_new, counts, "counts")
+        q = self.qbar
+        if _signature(q) != self._seen.get("qbar"):
+            s = self._shape
+            if not _need(q, "qbar", self.device, torch.float32, (s["h_kv"], s["d_h"])).is_contiguous():
+                raise ValueError("qbar must be contiguous")
+            self._seen["qbar"] = _signature(q)
+        rc = self._lib.dash_append_q4(p, self.kv, k_new.data_ptr(), v_new.data_ptr(), n,
+                                      None if counts is None else counts.data_ptr(), q.data_ptr(), self.kbar.data_ptr(),
+                                      self.state.data_ptr(), self.seqlens.data_ptr(), _current(self._index))
+        if rc:
+            L._check(rc, "dash_append_q4")
 
     def fill(self, K0, V0, lengths, stream=None):
         """Start over with the first lengths[b] tokens of K0, V0 [batch, n, h_kv, d]."""
         with _within(self.device, stream):
-            lengths = torch.as_tensor(lengths, dtype=torch.int32).to(self.device)
+            lengths = torch.as_tensor(lengths, dtype=torch.int32).to(self.device).contiguous()
+            self._check("append", K0, V0, lengths, "lengths")
             self.seqlens.zero_()
             self.append(K0, V0, lengths)
 
     def load(self, start, n, K=None, V=None, stream=None):
         """Positions start[b] .. start[b] + n - 1 (start: a number or device int32 [batch]) in bf16:
         K, V [batch, n, h_kv, d], zeros where nothing is cached."""
-        s = self._shape
-        per = isinstance(start, torch.Tensor)
-        if per and not _need(start, "start", self.device, torch.int32, self.seqlens.shape).is_contiguous():
-            raise ValueError("start must be contiguous")
-        with _within(self.device, stream):
-            if K is None:
-                K = torch.empty((s["batch"], n, s["h_kv"], s["d_h"]), dtype=torch.bfloat16, device=self.device)
-            if V is None:
-                V = torch.empty((s["batch"], n, s["h_kv"], s["d_h"]), dtype=torch.bfloat16, device=self.device)
-            K, V = self._tokens(K, "K"), self._tokens(V, "V")
-            if K.shape[1] != n or V.shape[1] != n:
-                raise ValueError(f"K and V must hold {n} tokens")
-            L.dash_load_q4(self._params(K, V), self.kv, start if per else None, 0 if per else start, n, self.seqlens, K, V)
+        if _elsewhere(self._index, stream):
+            with _within(self.device, stream):
+                return self.load(start, n, K, V)
+        if K is None or V is None:
+            s = self._shape
+            shape = (s["batch"], n, s["h_kv"], s["d_h"])
+            K = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if K is None else K
+            V = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if V is None else V
+        rows = start if isinstance(start, torch.Tensor) else None
+        p, m = self._check("load", K, V, rows, "start")
+        if m != n:
+            raise ValueError(f"K and V must hold {n} tokens")
+        rc = self._lib.dash_load_q4(p, self.kv, None if rows is None else rows.data_ptr(), 0 if rows is not None else start, n,
+                                    self.seqlens.data_ptr(), K.data_ptr(), V.data_ptr(), _current(self._index))
+        if rc:
+            L._check(rc, "dash_load_q4")
         return K, V
 
     def decode(self, q, stream=None):
         """Attention of the query q [batch, h_q, d] of each sequence's last token; zeros for an empty one."""
-        _need(q, "q", self.device, torch.bfloat16, self.O.shape)
-        if not q.is_contiguous():
-            raise ValueError("q must be contiguous")
-        with _within(self.device, stream):
-            L.dash_decode_q4(self.p, self.kv, q, self.kbar, self.seqlens, self.O, self.route, self.workspace)
+        if _elsewhere(self._index, stream):
+            with _within(self.device, stream):
+                return self.decode(q)
+        if _signature(q) != self._seen.get("q"):
+            if not _need(q, "q", self.device, torch.bfloat16, self.O.shape).is_contiguous():
+                raise ValueError("q must be contiguous")
+            self._seen["q"] = _signature(q)
+        rc = self._lib.dash_decode_q4(self.p, self.kv, q.data_ptr(), self.kbar.data_ptr(), self.seqlens.data_ptr(),
+                                      self.O.data_ptr(), self.route, self.workspace.data_ptr(), self._ws_bytes,
+                                      _current(self._index))
+        if rc:
+            L._check(rc, "dash_decode_q4")
         return self.O
 
     def step(self, q, k_new, v_new, stream=None):
@@ -174,6 +213,9 @@ class PagePool:
 
     def __init__(self, page_table, refs, seqlens, *, page_size):
         self.device = page_table.device
+        self._index = self.device.index
+        self._lib = L.load()
+        self._seen = {}
         for t, name, dim in ((page_table, "page_table", 2), (refs, "refs", 1), (seqlens, "seqlens", 1)):
             _need(t, name, self.device, torch.int32)
             if t.dim() != dim or not t.is_contiguous():
@@ -187,6 +229,7 @@ class PagePool:
         self._describe()
         ws = L.dash_pages_workspace_size(self.pg)
         self.workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=self.device)
+        self._ws = (self.workspace.data_ptr(), self.workspace.shape[0])
 
     @classmethod
     def of(cls, states):
@@ -258,51 +301,73 @@ class PagePool:
         self._kept.append(t)
 
     def _list(self, v, name):
-        if isinstance(v, torch.Tensor):
+        """A list of indices as a device int32 tensor."""
+        if not isinstance(v, torch.Tensor):
+            return torch.tensor(list(v), dtype=torch.int32).to(self.device)
+        if self._seen.get(name) != _signature(v):
             if v.dim() != 1 or not _need(v, name, self.device, torch.int32).is_contiguous():
                 raise ValueError(f"{name}: a contiguous list is needed")
-            return v
-        return torch.tensor(list(v), dtype=torch.int32).to(self.device)
+            self._seen[name] = _signature(v)
+        return v
 
-    def _pair(self, src, dst):
+    def _pair(self, call, name, src, dst):
         src, dst = self._list(src, "src"), self._list(dst, "dst")
-        if src.shape != dst.shape:
+        n = src.shape[0]
+        if dst.shape[0] != n:
             raise ValueError("src and dst have different lengths")
-        return src, dst
+        rc = call(self.pg, src.data_ptr(), dst.data_ptr(), n, self.status.data_ptr(), *self._ws, _current(self._index))
+        if rc:
+            L._check(rc, name)
 
     def copy(self, src, dst, stream=None):
         """Copy the contents of pages src[i] to pages dst[i] (lists or device int32) in every pool."""
-        with _within(self.device, stream):
-            src, dst = self._pair(src, dst)
-            L.dash_pages_copy(self.pg, src, dst, src.shape[0], self.status, self.workspace, self.workspace.shape[0])
+        if _elsewhere(self._index, stream):
+            with _within(self.device, stream):
+                return self.copy(src, dst)
+        self._pair(self._lib.dash_pages_copy, "dash_pages_copy", src, dst)
 
     def reserve(self, count=1, stream=None):
         """Give rows the pages they lack for `count` more tokens (a number, or device int32 [batch])."""
-        with _within(self.device, stream):
-            per = None
-            if isinstance(count, torch.Tensor):
-                per, count = _need(count, "count", self.device, torch.int32, self.seqlens.shape), 0
-                if not per.is_contiguous():
-                    raise ValueError("count must be contiguous")
-            L.dash_pages_reserve(self.pg, per, count, self.status, self.workspace, self.workspace.shape[0])
+        if _elsewhere(self._index, stream):
+            with _within(self.device, stream):
+                return self.reserve(count)
+        per = None
+        if isinstance(count, torch.Tensor):
+            per = self._list(count, "count")
+            if per.shape != self.seqlens.shape:
+                raise ValueError("count: one number per row is needed")
+        rc = self._lib.dash_pages_reserve(self.pg, None if per is None else per.data_ptr(), 0 if per is not None else count,
+                                          self.status.data_ptr(), *self._ws, _current(self._index))
+        if rc:
+            L._check(rc, "dash_pages_reserve")
 
     def fork(self, src, dst, stream=None):
         """Make the empty rows dst[i] copies of the rows src[i]: full pages are shared, the last one is
         copied, summaries, states and lengths too."""
-        with _within(self.device, stream):
-            src, dst = self._pair(src, dst)
-            L.dash_pages_fork(self.pg, src, dst, src.shape[0], self.status, self.workspace, self.workspace.shape[0])
+        if _elsewhere(self._index, stream):
+            with _within(self.device, stream):
+                return self.fork(src, dst)
+        self._pair(self._lib.dash_pages_fork, "dash_pages_fork", src, dst)
 
     def free(self, rows, stream=None):
         """Empty the rows: pages nobody else holds become free."""
-        with _within(self.device, stream):
-            rows = self._list(rows, "rows")
-            L.dash_pages_free(self.pg, rows, rows.shape[0], self.status)
+        if _elsewhere(self._index, stream):
+            with _within(self.device, stream):
+                return self.free(rows)
+        rows = self._list(rows, "rows")
+        rc = self._lib.dash_pages_free(self.pg, rows.data_ptr(), rows.shape[0], self.status.data_ptr(),
+                                       _current(self._index))
+        if rc:
+            L._check(rc, "dash_pages_free")
 
     def compact(self, stream=None):
         """Move the used pages together at the front of the pools; returns their number (device int32)."""
-        with _within(self.device, stream):
-            L.dash_pages_compact(self.pg, self.used, self.workspace, self.workspace.shape[0])
+        if _elsewhere(self._index, stream):
+            with _within(self.device, stream):
+                return self.compact()
+        rc = self._lib.dash_pages_compact(self.pg, self.used.data_ptr(), *self._ws, _current(self._index))
+        if rc:
+            L._check(rc, "dash_pages_compact")
         return self.used
 
     def check(self):

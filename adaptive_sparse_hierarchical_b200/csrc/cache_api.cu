@@ -236,6 +236,7 @@ int dash_pages_fork(const dash_pages* pg, const int* src, const int* dst, int n,
     int rc = check_pages(pg);
     if (rc != DASH_OK) return rc;
     if (n < 0 || n > pg->batch || (n && (!src || !dst))) return DASH_EINVAL;
+    if (n > pages_max_fork()) return DASH_EUNSUPPORTED;
     if (!on(src, 4) || !on(dst, 4) || !on(status, 4)) return DASH_EALIGN;
     PagesWs w;
     if ((rc = check_ws(pg, workspace, ws_bytes, &w)) != DASH_OK) return rc;

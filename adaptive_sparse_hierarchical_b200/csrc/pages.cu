@@ -7,7 +7,7 @@
 // workspace; the mover spreads the list's bytes over the whole GPU.  A request that fails its
 // checks leaves an empty list, so nothing changes.  The mover is bound by HBM (2 bytes moved per
 // byte of a page); small requests by the two launches, which overlap (programmatic dependent
-// launch).
+// launch).  A copy of at most kFew pages needs no plan: every mover block checks the list itself.
 #include "q4.cuh"
 #include "pages.cuh"
 
@@ -18,6 +18,8 @@ constexpr int kPlan = 1024;             // threads of a plan block
 constexpr int kMove = 256;              // threads of a mover block
 constexpr long long kSeg = 8192;        // bytes a mover block takes at a time: two 16-byte loads per thread in flight
 constexpr int kSlots = 1024;            // table entries it takes at a time
+constexpr int kFew = 256;               // a list short enough for every block to check
+constexpr int kMarks = 4096;            // rows whose marks fit a plan's shared memory
 
 // Workspace header, then the lists (see PagesWs).
 struct Plan {
@@ -78,21 +80,28 @@ __device__ int block_scan(int v, int* total)
 
 constexpr int kPer = 8;   // pages a thread looks at per step
 
+// Bit k: page p0 + kPer * thread + k is free.
+__device__ __forceinline__ unsigned free_mask(const int* refs, int pages, int p0)
+{
+    const int p = p0 + threadIdx.x * kPer;
+    unsigned m = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+        if (p + k < pages && refs[p + k] == 0) m |= 1u << k;
+    return m;
+}
+
 // The `want` lowest pages with refs == 0, ascending, into list; returns how many there are (at most
-// want).  Called by the whole plan block.
-__device__ int lowest_free(const int* refs, int pages, int want, int* list)
+// want).  Called by the whole plan block; first = free_mask of the first step, loaded ahead.
+__device__ int lowest_free(const int* refs, int pages, int want, int* list, unsigned first)
 {
     int found = 0;
     for (int p0 = 0; p0 < pages && found < want; p0 += kPlan * kPer) {
-        const int p = p0 + threadIdx.x * kPer;
-        unsigned m = 0;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k)
-            if (p + k < pages && refs[p + k] == 0) m |= 1u << k;
+        unsigned m = p0 ? free_mask(refs, pages, p0) : first;
         int total;
         int at = found + block_scan(__popc(m), &total);
         for (; m; m &= m - 1, ++at)
-            if (at < want) list[at] = p + __ffs(m) - 1;
+            if (at < want) list[at] = p0 + threadIdx.x * kPer + __ffs(m) - 1;
         found += total;
     }
     __syncthreads();
@@ -133,6 +142,7 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(PageTab t, const int* co
 {
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned first = free_mask(t.refs, t.num_pages, 0);
     unsigned bad = 0;
     auto slots = [&](int b, int* s0, int* s1) {
         const int L = t.seqlens[b], add = counts ? counts[b] : count;
@@ -161,7 +171,7 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(PageTab t, const int* co
     }
     __syncthreads();
     if (want == 0) return;
-    if (want > t.num_pages || lowest_free(t.refs, t.num_pages, want, w.dst) < want) {
+    if (want > t.num_pages || lowest_free(t.refs, t.num_pages, want, w.dst, first) < want) {
         if (threadIdx.x == 0) fail(status, DASH_PAGES_FULL);
         return;
     }
@@ -183,54 +193,58 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(PageTab t, const int* co
 }
 
 // fork: checks, a page for every child whose parent ends inside one.  Leaves the parent's length
-// (w.row) and the child's own page (w.own, -1) per entry: the mover writes tables and lengths.
+// (w.row) and the child's own page (w.own, -1) per entry: the mover writes tables and lengths.  One
+// thread per entry (n <= kPlan).
 __global__ void __launch_bounds__(kPlan) plan_fork_kernel(PageTab t, const int* src, const int* dst, int n, int* status,
                                                           PagesWs w)
 {
+    __shared__ int marks[kMarks], fresh[kPlan];
     pdl_launch_dependents();
     Plan* plan = reinterpret_cast<Plan*>(w.head);
+    // the entry that writes a row; rows without one hold anything, which the look-up below recognises
+    int* mark = t.batch <= kMarks ? marks : w.mark;
+    const int i = threadIdx.x;
+    const bool on = i < n;
+    const int s = on ? src[i] : 0, d = on ? dst[i] : 0;
+    const unsigned first = free_mask(t.refs, t.num_pages, 0);
+    const bool inside = s >= 0 && s < t.batch && d >= 0 && d < t.batch;
     unsigned bad = 0;
-    for (int i = threadIdx.x; i < n; i += kPlan) {
-        const int s = src[i], d = dst[i];
-        if (s < 0 || s >= t.batch || d < 0 || d >= t.batch) { bad |= 1u << DASH_PAGES_INDEX; continue; }
-        w.mark[d] = i;
-        const int L = t.seqlens[s];
-        if (L < 0 || L > (long long)t.max_pages * t.page_size) { bad |= 1u << DASH_PAGES_LENGTH; continue; }
-        if (t.seqlens[d] != 0 || t.page_table[(long long)d * t.max_pages] >= 0) bad |= 1u << DASH_PAGES_BUSY;
-        w.row[i] = L;
+    int L = 0;
+    if (on && !inside) bad |= 1u << DASH_PAGES_INDEX;
+    if (on && inside) {
+        mark[d] = i;
+        L = t.seqlens[s];
+        const int Ld = t.seqlens[d], held = t.page_table[(long long)d * t.max_pages];
+        if (L < 0 || L > (long long)t.max_pages * t.page_size) bad |= 1u << DASH_PAGES_LENGTH;
+        else if (Ld != 0 || held >= 0) bad |= 1u << DASH_PAGES_BUSY;
     }
-    int code = first_failure(bad, status), want = 0;
+    int code = first_failure(bad, status), want = 0, at = 0, part = 0;
     if (!code) {
-        for (int i0 = 0; i0 < n; i0 += kPlan) {
-            const int i = i0 + threadIdx.x;
-            int part = 0, pg = -1;
-            if (i < n) {
-                const int k = w.mark[src[i]];
-                if (w.mark[dst[i]] != i || (k >= 0 && k < n && dst[k] == src[i])) bad |= 1u << DASH_PAGES_TWICE;
-                const int L = w.row[i];
-                part = L % t.page_size != 0;
-                if (part) {
-                    pg = t.page_table[(long long)src[i] * t.max_pages + L / t.page_size];
-                    if (pg < 0 || pg >= t.num_pages) bad |= 1u << DASH_PAGES_INDEX;
-                }
+        int pg = -1;
+        if (on) {
+            const int k = mark[s];
+            if (mark[d] != i || (k >= 0 && k < n && dst[k] == s)) bad |= 1u << DASH_PAGES_TWICE;
+            part = L % t.page_size != 0;
+            if (part) {
+                pg = t.page_table[(long long)s * t.max_pages + L / t.page_size];
+                if (pg < 0 || pg >= t.num_pages) bad |= 1u << DASH_PAGES_INDEX;
             }
-            int total;
-            const int at = want + block_scan(part, &total);
-            if (i < n) w.own[i] = part ? at : -1;
-            if (part) w.src[at] = pg;
-            want += total;
         }
+        at = block_scan(part, &want);
+        if (part) w.src[at] = pg;
         code = first_failure(bad, status);
     }
-    if (!code && want && (want > t.num_pages || lowest_free(t.refs, t.num_pages, want, w.dst) < want))
+    if (!code && want && (want > t.num_pages || lowest_free(t.refs, t.num_pages, want, fresh, first) < want))
         code = first_failure(1u << DASH_PAGES_FULL, status);
-    if (!code)
-        for (int i = threadIdx.x; i < n; i += kPlan)
-            if (w.own[i] >= 0) {
-                w.own[i] = w.dst[w.own[i]];
-                t.refs[w.own[i]] = 1;
-            }
-    if (threadIdx.x == 0) { plan->pairs = code ? 0 : want; plan->ok = !code; }
+    if (!code && on) {
+        w.row[i] = L;
+        w.own[i] = part ? fresh[at] : -1;
+        if (part) {
+            w.dst[at] = fresh[at];
+            t.refs[fresh[at]] = 1;
+        }
+    }
+    if (i == 0) { plan->pairs = code ? 0 : want; plan->ok = !code; }
 }
 
 // compact: U = pages in use; the k-th free page below U receives the k-th used page from U on.
@@ -281,13 +295,14 @@ __global__ void __launch_bounds__(kPlan) plan_compact_kernel(PageTab t, int* use
 }
 
 // ---- mover --------------------------------------------------------------------------------------------
-// Work of one launch, taken unit by unit: first the listed pages of up to kArrays arrays (pieces of
-// kSeg bytes), then, for a fork, the rows of up to kArrays row arrays, then the tables.
+// Work of one launch, taken unit by unit: first the listed pages of up to CAP arrays (pieces of
+// kSeg bytes), then, for a fork, the rows of up to CAP row arrays, then the tables.
 enum { MOVE_PAGES = 0, MOVE_FORK = 1, MOVE_COMPACT = 2 };
 
+template <int CAP>
 struct Move {
-    MoveArray pages[kArrays];
-    MoveRows rows[kArrays];
+    MoveArray pages[CAP];
+    MoveRows rows[CAP];
     int np, nr, segs;               // arrays, row arrays, pieces per page over all arrays
     long long row_units;            // pieces per forked row over all row arrays
     int op, n;                      // fork: entries
@@ -315,7 +330,49 @@ __device__ __forceinline__ void copy_bytes(char* dst, const char* src, long long
 }
 static_assert(kSeg == 2 * 16 * kMove, "a piece is two vectors per thread");
 
-__global__ void __launch_bounds__(kMove) move_kernel(PageTab t, PagesWs w, const __grid_constant__ Move mv)
+// Piece q of page `from` to page `to`.
+template <int CAP>
+__device__ __forceinline__ void copy_piece(const Move<CAP>& mv, int from, int to, int q)
+{
+    int a = 0;
+    while (q >= mv.pages[a].segs) q -= mv.pages[a++].segs;
+    const MoveArray& m = mv.pages[a];
+    const long long off = q * kSeg;
+    copy_bytes(m.data + (long long)to * m.stride + off, m.data + (long long)from * m.stride + off, min(kSeg, m.bytes - off),
+               true);
+}
+
+// Copy of n <= kFew pages: every block checks the whole list (the rules of plan_copy_kernel).
+template <int CAP>
+__global__ void __launch_bounds__(kMove) copy_few_kernel(PageTab t, const int* src, const int* dst, int n, int* status,
+                                                         const __grid_constant__ Move<CAP> mv)
+{
+    __shared__ int from[kFew], to[kFew];
+    __shared__ unsigned all;
+    pdl_launch_dependents();
+    const int i = threadIdx.x;
+    static_assert(kFew <= kMove, "one thread per entry");
+    if (i == 0) all = 0;
+    if (i < n) { from[i] = src[i]; to[i] = dst[i]; }
+    __syncthreads();
+    if (i < n) {
+        const int s = from[i], d = to[i];
+        unsigned bad = s < 0 || s >= t.num_pages || d < 0 || d >= t.num_pages ? 1u << DASH_PAGES_INDEX : 0u;
+        for (int k = 0; k < n; ++k)
+            if ((k != i && to[k] == d) || (to[k] == s && from[k] != s)) bad |= 1u << DASH_PAGES_TWICE;
+        if (bad) atomicOr(&all, bad);
+    }
+    __syncthreads();
+    if (all) {
+        if (blockIdx.x == 0 && i == 0) fail(status, __ffs(all) - 1);
+        return;
+    }
+    for (long long u = blockIdx.x; u < (long long)n * mv.segs; u += gridDim.x)
+        copy_piece(mv, from[u / mv.segs], to[u / mv.segs], (int)(u % mv.segs));
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kMove) move_kernel(PageTab t, PagesWs w, const __grid_constant__ Move<CAP> mv)
 {
     pdl_wait();   // the plan
     pdl_launch_dependents();
@@ -329,12 +386,7 @@ __global__ void __launch_bounds__(kMove) move_kernel(PageTab t, PagesWs w, const
     for (long long u = blockIdx.x; u < total; u += gridDim.x) {
         if (u < page_units) {
             const int k = (int)(u / mv.segs);
-            int q = (int)(u % mv.segs), a = 0;
-            while (q >= mv.pages[a].segs) q -= mv.pages[a++].segs;
-            const MoveArray& m = mv.pages[a];
-            const long long off = q * kSeg;
-            copy_bytes(m.data + (long long)w.dst[k] * m.stride + off, m.data + (long long)w.src[k] * m.stride + off,
-                       min(kSeg, m.bytes - off), true);
+            copy_piece(mv, w.src[k], w.dst[k], (int)(u % mv.segs));
         } else if (u < page_units + row_units) {
             const long long v = u - page_units;
             const int k = (int)(v / mv.row_units);
@@ -384,12 +436,14 @@ __global__ void __launch_bounds__(kMove) move_kernel(PageTab t, PagesWs w, const
 }
 
 // free: one block per (entry, part of its row); of equal entries the first acts.
+template <int CAP>
 struct Clear {
-    MoveRows rows[kArrays];
+    MoveRows rows[CAP];
     int n, tables;
 };
+template <int CAP>
 __global__ void __launch_bounds__(kMove) free_kernel(PageTab t, const int* rows, int n, int* status,
-                                                     const __grid_constant__ Clear c)
+                                                     const __grid_constant__ Clear<CAP> c)
 {
     const int i = blockIdx.x, b = rows[i];
     if (b < 0 || b >= t.batch) {
@@ -441,21 +495,22 @@ dim3 move_grid(long long units)
     return dim3((unsigned)(units < 1 ? 1 : units < most ? units : most));
 }
 
-// The mover's launches: the arrays in groups of kArrays.
-cudaError_t launch_move(const PageTab& t, const PagesWs& w, const dash_pages* pg, int op, int n, const int* src,
-                        const int* dst, long long most_pairs, cudaStream_t st)
+// The mover's launches: the arrays in groups of CAP.
+template <int CAP>
+cudaError_t move_groups(const PageTab& t, const PagesWs* w, const dash_pages* pg, int op, int n, const int* src,
+                        const int* dst, int* status, long long most_pairs, cudaStream_t st)
 {
     int a = 0, r = 0;
     bool first = true;
     const int nr = op == MOVE_FORK ? pg->num_rows : 0;
     while (first || a < pg->num_arrays || r < nr) {
-        Move mv = {};
+        Move<CAP> mv = {};
         mv.op = op;
         mv.n = n;
         mv.src = src;
         mv.dst = dst;
         mv.tables = first && op != MOVE_PAGES;
-        for (; a < pg->num_arrays && mv.np < kArrays; ++a) {
+        for (; a < pg->num_arrays && mv.np < CAP; ++a) {
             const dash_page_array& p = pg->arrays[a];
             if (p.page_bytes == 0) continue;
             MoveArray& m = mv.pages[mv.np++];
@@ -465,22 +520,56 @@ cudaError_t launch_move(const PageTab& t, const PagesWs& w, const dash_pages* pg
             m.segs = (int)((p.page_bytes + kSeg - 1) / kSeg);
             mv.segs += m.segs;
         }
-        for (; r < nr && mv.nr < kArrays; ++r) {
+        for (; r < nr && mv.nr < CAP; ++r) {
             const dash_row_array& p = pg->rows[r];
             if (p.unit_bytes == 0 || p.heads == 0 || p.max_units == 0) continue;
             const MoveRows& m = mv.rows[mv.nr++] = rows_of(p);
             mv.row_units += (long long)m.heads * m.segs;
         }
-        const long long tab = mv.tables ? (long long)(op == MOVE_FORK ? n : t.batch) * ((t.max_pages + kSlots - 1) / kSlots) : 0;
-        const cudaError_t e = launch_after(move_kernel, move_grid(most_pairs * mv.segs + mv.row_units * n + tab),
-                                           dim3(kMove), 0, st, t, w, mv);
+        cudaError_t e;
+        if (!w) {
+            if (mv.segs == 0) break;
+            copy_few_kernel<CAP><<<move_grid(most_pairs * mv.segs), kMove, 0, st>>>(t, src, dst, n, status, mv);
+            e = cudaGetLastError();
+        } else {
+            const long long tab = mv.tables ? (long long)(op == MOVE_FORK ? n : t.batch) * ((t.max_pages + kSlots - 1) / kSlots) : 0;
+            e = launch_after(move_kernel<CAP>, move_grid(most_pairs * mv.segs + mv.row_units * n + tab), dim3(kMove), 0, st,
+                             t, *w, mv);
+        }
         if (e != cudaSuccess) return e;
         first = false;
     }
     return cudaSuccess;
 }
 
+// w: the plan's lists; null for a copy without a plan (src, dst are its lists).
+cudaError_t launch_move(const PageTab& t, const PagesWs* w, const dash_pages* pg, int op, int n, const int* src,
+                        const int* dst, int* status, long long most_pairs, cudaStream_t st)
+{
+    // few arrays travel in a small argument block: the launch is cheaper
+    return pg->num_arrays <= kFewArrays && pg->num_rows <= kFewArrays
+               ? move_groups<kFewArrays>(t, w, pg, op, n, src, dst, status, most_pairs, st)
+               : move_groups<kArrays>(t, w, pg, op, n, src, dst, status, most_pairs, st);
+}
+
+template <int CAP>
+cudaError_t free_groups(const PageTab& t, const dash_pages* pg, const int* rows, int n, int* status, cudaStream_t st)
+{
+    int r = 0;
+    for (bool first = true; first || r < pg->num_rows; first = false) {
+        Clear<CAP> c = {};
+        c.tables = first;
+        for (; r < pg->num_rows && c.n < CAP; ++r)
+            if (pg->rows[r].clear) c.rows[c.n++] = rows_of(pg->rows[r]);
+        if (!first && c.n == 0) break;
+        free_kernel<CAP><<<dim3(n, first ? (t.max_pages + kSlots - 1) / kSlots : 1), kMove, 0, st>>>(t, rows, n, status, c);
+    }
+    return cudaGetLastError();
+}
+
 }  // namespace
+
+int pages_max_fork() { return kPlan; }
 
 size_t pages_ws(const PageTab& t, char* base, PagesWs* w)
 {
@@ -503,9 +592,10 @@ size_t pages_ws(const PageTab& t, char* base, PagesWs* w)
 cudaError_t launch_pages_copy(const PageTab& t, const dash_pages* pg, const int* src, const int* dst, int n, int* status,
                               const PagesWs& w, cudaStream_t st)
 {
+    if (n <= kFew) return launch_move(t, nullptr, pg, MOVE_PAGES, n, src, dst, status, n, st);
     plan_copy_kernel<<<1, kPlan, 0, st>>>(t, src, dst, n, status, w);
     const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_move(t, w, pg, MOVE_PAGES, 0, nullptr, nullptr, n, st);
+    return e != cudaSuccess ? e : launch_move(t, &w, pg, MOVE_PAGES, 0, nullptr, nullptr, nullptr, n, st);
 }
 
 cudaError_t launch_pages_reserve(const PageTab& t, const int* counts, int count, int* status, const PagesWs& w,
@@ -520,28 +610,20 @@ cudaError_t launch_pages_fork(const PageTab& t, const dash_pages* pg, const int*
 {
     plan_fork_kernel<<<1, kPlan, 0, st>>>(t, src, dst, n, status, w);
     const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_move(t, w, pg, MOVE_FORK, n, src, dst, n, st);
+    return e != cudaSuccess ? e : launch_move(t, &w, pg, MOVE_FORK, n, src, dst, nullptr, n, st);
 }
 
 cudaError_t launch_pages_free(const PageTab& t, const dash_pages* pg, const int* rows, int n, int* status, cudaStream_t st)
 {
-    int r = 0;
-    for (bool first = true; first || r < pg->num_rows; first = false) {
-        Clear c = {};
-        c.tables = first;
-        for (; r < pg->num_rows && c.n < kArrays; ++r)
-            if (pg->rows[r].clear) c.rows[c.n++] = rows_of(pg->rows[r]);
-        if (!first && c.n == 0) break;
-        free_kernel<<<dim3(n, first ? (t.max_pages + kSlots - 1) / kSlots : 1), kMove, 0, st>>>(t, rows, n, status, c);
-    }
-    return cudaGetLastError();
+    return pg->num_rows <= kFewArrays ? free_groups<kFewArrays>(t, pg, rows, n, status, st)
+                                      : free_groups<kArrays>(t, pg, rows, n, status, st);
 }
 
 cudaError_t launch_pages_compact(const PageTab& t, const dash_pages* pg, int* used, const PagesWs& w, cudaStream_t st)
 {
     plan_compact_kernel<<<1, kPlan, 0, st>>>(t, used, w);
     const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_move(t, w, pg, MOVE_COMPACT, 0, nullptr, nullptr, t.num_pages / 2, st);
+    return e != cudaSuccess ? e : launch_move(t, &w, pg, MOVE_COMPACT, 0, nullptr, nullptr, nullptr, t.num_pages / 2, st);
 }
 
 }  // namespace dash

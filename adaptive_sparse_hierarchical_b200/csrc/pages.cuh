@@ -5,7 +5,7 @@
 
 namespace dash {
 
-constexpr int kArrays = 64;   // arrays per mover launch (they travel as kernel arguments)
+constexpr int kArrays = 64, kFewArrays = 8;   // arrays per mover launch (they travel as kernel arguments)
 
 struct PageTab {
     int batch, max_pages, page_size, num_pages;
@@ -31,6 +31,7 @@ struct PagesWs {
     char* head;
     int *src, *dst, *mark, *row, *own;
 };
+int pages_max_fork();   // entries of one fork call
 size_t pages_ws(const PageTab& t, char* base, PagesWs* w);   // carves `base` up; returns the bytes needed
 
 cudaError_t launch_pages_copy(const PageTab& t, const dash_pages* pg, const int* src, const int* dst, int n, int* status,

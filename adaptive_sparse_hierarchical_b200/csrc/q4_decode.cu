@@ -40,6 +40,9 @@ namespace dash {
 namespace {
 
 constexpr int kMaxPairs = 2048;
+constexpr int kMaxBlocks = 1024;
+// Granules that a second pair costs a block, in time: about 5 us against 2.4 us per round of its warps.
+constexpr int kTurn = 32;
 constexpr int kMeta = 64;         // granule descriptors per warp (two halves of 32)
 
 // Descriptor of a granule: where its codes and scales lie, its chunk's bias, tokens | mapped << 8.
@@ -129,7 +132,7 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, 
     constexpr int OLD = St::OLD, kGran = St::GRAN, kStages = St::N;
     static_assert(8 * NT * OLD * 4 <= kStages * St::BYTES, "the merge buffer reuses a warp's ring");
     extern __shared__ __align__(128) char smem[];
-    __shared__ int pre[kMaxPairs + 1];
+    __shared__ int pre[kMaxPairs + 1], first_blk[kMaxBlocks + 1], own_blocks;
     __shared__ float mrg_m[W][8 * NT], mrg_l[W][8 * NT], mrg_s[W][8 * NT], tot_m[8 * NT], tot_l[8 * NT];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -159,12 +162,69 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, 
     __syncthreads();
     const long long total = pre[BR];
     // every warp of a block in use has a granule
-    const int used = (int)min((long long)gridDim.x, (total + W - 1) / W);
+    int used = (int)min((long long)gridDim.x, (total + W - 1) / W);
+    // Blocks of their own for every pair, if that costs no block more than kTurn granules over an even
+    // share: a second pair in a block costs a merge, a descriptor chase and an empty ring.
+    if (warp == 0) {
+        int cap = 0;
+        if (BR <= used && total > 2ll * W * used) {   // (not for a round or two per warp)
+            auto blocks = [&](int m) {   // blocks needed when none takes more than m granules
+                int n = 0;
+                for (int x = lane; x < BR; x += 32) n += (pre[x + 1] - pre[x] + m - 1) / m;
+                return warp_isum(n);
+            };
+            int lo_c = (int)((total + used - 1) / used), hi_c = lo_c + kTurn;
+            if (blocks(hi_c) <= used) {
+                while (lo_c < hi_c) {
+                    const int m = (lo_c + hi_c) >> 1;
+                    if (blocks(m) <= used) hi_c = m;
+                    else lo_c = m + 1;
+                }
+                cap = hi_c;
+                int run = 0;
+                for (int x0 = 0; x0 < BR; x0 += 32) {
+                    const int x = x0 + lane;
+                    int v = x < BR ? (pre[x + 1] - pre[x] + cap - 1) / cap : 0;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int u = __shfl_up_sync(0xffffffffu, v, o);
+                        if (lane >= o) v += u;
+                    }
+                    if (x < BR) first_blk[x + 1] = run + v;
+                    run += __shfl_sync(0xffffffffu, v, 31);
+                }
+                if (lane == 0) first_blk[0] = 0;
+            }
+        }
+        if (lane == 0) own_blocks = cap > 0;
+    }
+    __syncthreads();
+    int lo, hi, x = 0;
+    auto last_le = [&](const int* v, int k) {   // the x with v[x] <= k < v[x + 1]
+        int l = 0, h = BR;
+        while (l < h) {
+            const int m = (l + h) >> 1;
+            if (v[m + 1] <= k) l = m + 1;
+            else h = m;
+        }
+        return l;
+    };
+    if (own_blocks) used = first_blk[BR];
     if (blockIdx.x == 0)
         for (int x = threadIdx.x; x < BR; x += 32 * W)
             if (pre[x] == pre[x + 1]) a.span[x] = make_int2(0, -1);
     if ((int)blockIdx.x >= used) return;
-    const int lo = (int)(total * blockIdx.x / used), hi = (int)(total * (blockIdx.x + 1) / used);
+    if (own_blocks) {
+        x = last_le(first_blk, blockIdx.x);
+        const int k = first_blk[x + 1] - first_blk[x], j = blockIdx.x - first_blk[x];
+        const long long n = pre[x + 1] - pre[x];
+        lo = pre[x] + (int)(n * j / k);
+        hi = pre[x] + (int)(n * (j + 1) / k);
+    } else {
+        lo = (int)(total * blockIdx.x / used);
+        hi = (int)(total * (blockIdx.x + 1) / used);
+        x = last_le(pre, lo);
+    }
 
     char* ring = smem + warp * (kStages * St::BYTES);
     const uint32_t ring_a = smem_u32(ring);
@@ -183,16 +243,6 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, 
     const int vw0 = v_at(vr0), vw1 = v_at(vr1);
     const int vs0 = St::VS + vr0 * NG + (D == 128 ? g >> 1 : g >> 2), vs1 = St::VS + vr1 * NG + (D == 128 ? g >> 1 : g >> 2);
 
-    int x = 0;
-    {   // first pair with granules in this block's range
-        int l = 0, h = BR;
-        while (l < h) {
-            const int m = (l + h) >> 1;
-            if (pre[m + 1] <= lo) l = m + 1;
-            else h = m;
-        }
-        x = l;
-    }
     for (; x < BR && pre[x] < hi; ++x) {
         const int p0 = pre[x], p1 = pre[x + 1];
         const int s_lo = max(lo, p0), s_hi = min(hi, p1);
@@ -586,15 +636,14 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, 
     }
 }
 
-// Pairs that span blocks (and zeros for empty sequences): one block per (pair, head) or per pair,
-// kMergeY partials at a time, weights first.
-constexpr int kMergeY = 8, kMaxBlocks = 1024;
+// Pairs that span blocks (and zeros for empty sequences): kMergeY groups of D threads (one per column)
+// take the pieces in turn, each with a running reference, and are then added in order.
+constexpr int kMergeY = 4;
 
 template <int D>
 __global__ void __launch_bounds__(D * kMergeY) q4_merge_kernel(Shape s, Attend a, int vexp)
 {
-    __shared__ float wt[kMaxBlocks], sums[kMaxBlocks], acc[kMergeY][D];
-    __shared__ float red[32];
+    __shared__ float acc[kMergeY][D], ms[kMergeY], ls[kMergeY];
     pdl_wait();
     const int x = blockIdx.x, G = s.g, col = threadIdx.x % D, y = threadIdx.x / D;
     const int2 sp = a.span[x];
@@ -602,48 +651,51 @@ __global__ void __launch_bounds__(D * kMergeY) q4_merge_kernel(Shape s, Attend a
     if (n == 1) return;   // finished in its block
     const int b = x / s.hkv, r = x % s.hkv;
     __nv_bfloat16* out = a.O + ((long long)b * s.hq + r * G) * D;
-    if (n == 0) {
-        for (int h = blockIdx.y; h < G; h += gridDim.y)
-            if (y == 0) out[h * D + col] = __float2bfloat16_rn(0.f);
-        return;
-    }
     const long long stride = (long long)G * (D + 2);
     for (int h = blockIdx.y; h < G; h += gridDim.y) {
-        // partial j: the last piece of block c0 (j = 0), the first piece of block c0 + j
+        // piece j: the last one of block c0 (j = 0), the first one of block c0 + j
         const float* base = a.part + (long long)h * (D + 2);
-        auto piece = [&](int j) { return base + ((long long)(c0 + j) * 2 + (j == 0 ? 1 : 0)) * stride; };
-        float M = -INFINITY;
-        for (int j = threadIdx.x; j < n; j += D * kMergeY) {
-            const float* p = piece(j);
-            wt[j] = p[D];
-            sums[j] = p[D + 1];
-            M = fmaxf(M, wt[j]);
-        }
-        M = warp_max(M);
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = M;
-        __syncthreads();
-        M = -INFINITY;
-        for (int w = 0; w < D * kMergeY / 32; ++w) M = fmaxf(M, red[w]);
-        for (int j = threadIdx.x; j < n; j += D * kMergeY) wt[j] = wt[j] == -INFINITY ? 0.f : exp2f(wt[j] - M);
-        __syncthreads();
-        float t = 0.f;
-        int j = y;
-        for (; j + 3 * kMergeY < n; j += 4 * kMergeY) {
-            float v[4];
+        float M = -INFINITY, L = 0.f, t = 0.f;
+        for (int j0 = y; j0 < n; j0 += 4 * kMergeY) {
+            float m[4], l[4], v[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = piece(j + u * kMergeY)[col];
+            for (int u = 0; u < 4; ++u) {
+                const int j = j0 + u * kMergeY;
+                const float* p = base + ((long long)(c0 + j) * 2 + (j == 0 ? 1 : 0)) * stride;
+                m[u] = j < n ? p[D] : -INFINITY;
+                l[u] = j < n ? p[D + 1] : 0.f;
+                v[u] = j < n ? p[col] : 0.f;
+            }
+            float top = M;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) t = fmaf(v[u], wt[j + u * kMergeY], t);
+            for (int u = 0; u < 4; ++u) top = fmaxf(top, m[u]);
+            const float f = M == -INFINITY ? 1.f : exp2f(M - top);   // nothing but NaNs so far: they stay
+            L *= f;
+            t *= f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float w = m[u] == -INFINITY ? 1.f : exp2f(m[u] - top);   // no reference: zeros or NaNs
+                L = fmaf(l[u], w, L);
+                t = fmaf(v[u], w, t);
+            }
+            M = top;
         }
-        for (; j < n; j += kMergeY) t = fmaf(piece(j)[col], wt[j], t);
         acc[y][col] = t;
+        if (col == 0) { ms[y] = M; ls[y] = L; }
         __syncthreads();
         if (y == 0) {
+            float top = M;
+#pragma unroll
+            for (int k = 1; k < kMergeY; ++k) top = fmaxf(top, ms[k]);
             float sum = 0.f;
-            for (int k = 0; k < n; ++k) sum = fmaf(sums[k], wt[k], sum);
             t = 0.f;
-            for (int k = 0; k < kMergeY; ++k) t += acc[k][col];
-            out[h * D + col] = __float2bfloat16_rn(t * (16.f * exp2i(vexp)) / sum);
+#pragma unroll
+            for (int k = 0; k < kMergeY; ++k) {
+                const float w = ms[k] == -INFINITY ? 1.f : exp2f(ms[k] - top);
+                sum = fmaf(ls[k], w, sum);
+                t = fmaf(acc[k][col], w, t);
+            }
+            out[h * D + col] = __float2bfloat16_rn(n ? t * (16.f * exp2i(vexp)) / sum : 0.f);
         }
         __syncthreads();
     }

@@ -118,7 +118,8 @@ int dash_pages_reserve(const dash_pages* pg, const int* counts, int count, int* 
 
 /* Row dst[i] (empty: length 0 and no pages) becomes a copy of row src[i], i < n (device int32): it
  * shares the pages that src has filled, gets its own copy of the page that src has filled in part,
- * and copies of src's entries in `rows`.  A source may occur several times. */
+ * and copies of src's entries in `rows`.  A source may occur several times.  At most 1024 entries
+ * per call. */
 int dash_pages_fork(const dash_pages* pg, const int* src, const int* dst, int n, int* status, void* workspace,
                     size_t ws_bytes, void* stream);
 
