@@ -148,11 +148,11 @@ class Q4DecodeState:
         if _elsewhere(self._index, stream):
             with _within(self.device, stream):
                 return self.load(start, n, K, V)
-        if K is None or V is None:
+        if K is None:
             s = self._shape
-            shape = (s["batch"], n, s["h_kv"], s["d_h"])
-            K = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if K is None else K
-            V = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if V is None else V
+            K = torch.empty((s["batch"], n, s["h_kv"], s["d_h"]), dtype=torch.bfloat16, device=self.device)
+        if V is None:
+            V = torch.empty_like(K, memory_format=torch.contiguous_format)
         rows = start if isinstance(start, torch.Tensor) else None
         p, m = self._check("load", K, V, rows, "start")
         if m != n:

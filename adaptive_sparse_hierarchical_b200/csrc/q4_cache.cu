@@ -1,17 +1,22 @@
 // q4_cache.cu -- writing and reading the 4-bit cache: append (quantisation fused with the Stage 0
 // summaries) and load.  Format and layout: include/dash_cache.h.
 //
-// Quantisation of a group of 32 elements x (4 lanes of 8): s = e4m3(max|x| 2^-e / 7), a true
-// division; u = round(x 2^-e / s) + 8.  With s rounded to nearest, max|x| / s < 7.5, so nothing is
-// clipped by more than half a step while s is a normal e4m3 number; below 2^-6 the clamp acts.
-// The quotient is formed as x * (2^-e / s) and must still round as the true quotient does.  x has
-// 8 significant bits and s has 4, so the quotient is either exactly half-way between two integers
-// or at least 2^-9 away from it; the product's error is below 2^-20.  Rounding the product to
-// multiples of 2^-13 first (adding and subtracting 1536) therefore restores exact ties and cannot
-// make new ones.
+// Quantisation of a group of 32 elements x (4 lanes of 8): s = e4m3(max|x| 2^-e / 7), u = round(x
+// 2^-e / s) + 8, both with the quotients' exact ties.  With s rounded to nearest, max|x| / s < 7.5, so
+// nothing is clipped by more than half a step while s is a normal e4m3 number below 448; the clamp
+// acts below 2^-6 and at 448.  Neither quotient needs a division:
+//   - max|x| / 7 has an 8-bit dividend, so it is a midpoint of e4m3 (5 bits) exactly or at least 2^-8
+//     of it away; the product with 1/7 is off by 2^-23, and rounding it to f16 (11 bits) first
+//     restores the midpoints and makes no new ones;
+//   - x has 8 significant bits and s has 4, so x / s is k + 1/2 exactly or at least (k + 1/2) / 256 away
+//     from it; x * (2^-e / s) is off by 2^-22 of itself, and rounding it to f16 first does the same.
+// Adding 1032 in f16 (two values at a time; the spacing there is 1) then leaves the code in the low bits,
+// and the sums are added up, shifted, with what their upper bits contribute taken off once.
 //
-// Bound: HBM for a prompt (2 bytes read and 17/32 written per element; a bulk block has K and V
-// rows in flight at once), launch latency for single tokens.
+// Bound: HBM for a prompt (2 bytes read and 17/32 written per element) with the instruction rate close
+// behind; launch latency for single tokens.
+#include <cuda_fp16.h>
+
 #include "q4.cuh"
 
 namespace dash {
@@ -25,30 +30,40 @@ struct Row {
     static constexpr int LPK = D / 8, KPI = 32 / LPK;
 };
 
-// Codes of the 8 elements of this lane and its group's scale byte (equal in the group's 4 lanes).
-// inv_e = 2^-e.  Every lane of the warp takes part.
-__device__ __forceinline__ uint32_t quant8(uint4 raw, float inv_e, uint32_t* scale)
+// Codes of the 8 elements x of this lane (raw: their bf16 bits) and its group's scale byte (equal in the
+// group's 4 lanes).  inv_e = 2^-e.  Every lane of the warp takes part.
+__device__ __forceinline__ uint32_t quant8(uint4 raw, const float* x, float inv_e, uint32_t* scale)
 {
     // |x| as bf16 bits: ordered as integers, infinities and NaNs on top
     uint32_t t = __vmaxu2(__vmaxu2(raw.x & 0x7fff7fffu, raw.y & 0x7fff7fffu),
                           __vmaxu2(raw.z & 0x7fff7fffu, raw.w & 0x7fff7fffu));
     t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, 1));
     t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, 2));
-    const uint32_t top = max(t & 0xffffu, t >> 16);
-    const float f = top < 0x7f80u ? __fdiv_rn(__uint_as_float(top << 16) * inv_e, 7.f) : __int_as_float(0x7fffffff);
-    const uint32_t sb = f32_to_e4m3(f);
-    *scale = sb;
-    const float s = e4m3_to_f32(sb);
-    const float r = s > 0.f ? __frcp_rn(s) * inv_e : 0.f;
-    float x[8];
-    Vec<__nv_bfloat16>::cvt(raw, x);
-    uint32_t w = 0;
+    const uint32_t top = max(t << 16, t & 0xffff0000u);   // as fp32 bits
+    const float f = top < 0x7f800000u ? __uint_as_float(top) * inv_e * (1.f / 7.f) : __int_as_float(0x7fffffff);
+    uint32_t sb, h;
+    float s, r;
+    asm("{\n\t.reg .b16 b;\n\tcvt.rn.f16x2.f32 %1, %2, %2;\n\tcvt.rn.satfinite.e4m3x2.f16x2 b, %1;\n\t"
+        "cvt.u32.u16 %0, b;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}\n"
+        : "=r"(sb), "=r"(h)
+        : "f"(f));
+    s = __half2float(__ushort_as_half((unsigned short)h));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    r = s == 0.f ? 0.f : r * inv_e;
+    *scale = sb = sb & 0xffu;
+    __half2 y[4];   // elements i and i + 4
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float y = __fadd_rn(fmaf(x[i], r, 1536.f), -1536.f);
-        y = fminf(fmaxf(y, -7.f), 7.f);
-        // 1.5 * 2^23 + 8: the low bits of the sum are round(y) + 8
-        w |= (__float_as_uint(__fadd_rn(y, 12582920.f)) & 15u) << (4 * i);
+    for (int i = 0; i < 4; ++i) y[i] = __floats2half2_rn(x[i] * r, x[i + 4] * r);
+    if (__any_sync(0xffffffffu, sb - 1u < 7u || sb == 0x7eu)) {   // a subnormal or the largest scale in the warp
+        const __half2 lo = __float2half2_rn(-7.f), hi = __float2half2_rn(7.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = __hmin2(__hmax2(y[i], lo), hi);
+    }
+    uint32_t w = 0u - 0x64006400u * 0x1111u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 u = __hadd2(y[i], __float2half2_rn(1032.f));
+        w += *reinterpret_cast<const uint32_t*>(&u) << (4 * i);
     }
     return w;
 }
@@ -133,7 +148,7 @@ __device__ __forceinline__ void write_summary(float* out, int sub, const Sum& r)
 // the first chunk also takes the chunk left open at the end, so that the state is read and written
 // by one block, in that order.
 template <int D>
-__global__ void __launch_bounds__(32 * kBulkWarps)
+__global__ void __launch_bounds__(32 * kBulkWarps, 4)
 append_bulk_kernel(Shape s, Q4 c, Append a)
 {
     using R = Row<D>;
@@ -156,39 +171,84 @@ append_bulk_kernel(Shape s, Q4 c, Append a)
 
     auto chunk = [&](int cc, bool with_state) {
         const int t0 = max(cc * s.B, L), t1 = min((cc + 1) * s.B, end);
+        // This lane's rows are first_row + i STEP of the chunk; the first ones are on their way before the page
+        // is known, the next ones before the present ones are worked on.
+        constexpr int U = 4, STEP = kBulkWarps * R::KPI;
+        const int first_row = warp * R::KPI + grp;
+        const __nv_bfloat16* kp = kb + (long long)(t0 - L + first_row) * s.ks[1];
+        const __nv_bfloat16* vp = vb + (long long)(t0 - L + first_row) * s.vs[1];
+        const long long kstep = STEP * s.ks[1], vstep = STEP * s.vs[1];
+        int left = t1 - t0 - first_row;   // row i is there while left > i STEP
+        uint4 kr[U], vr[U];
+        auto load = [&](int rows) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                kr[u] = vr[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (rows > u * STEP) {
+                    kr[u] = *reinterpret_cast<const uint4*>(kp);
+                    vr[u] = *reinterpret_cast<const uint4*>(vp);
+                }
+                kp += kstep;
+                vp += vstep;
+            }
+        };
+        load(left);
         const int pg = q4_page(c, b, t0);
-        const long long row0 = (long long)r * c.psz + t0 % c.psz;
-        uint8_t *kc = c.kc + pg * c.kcp, *ks = c.ks + pg * c.ksp, *vc = c.vc + pg * c.vcp, *vs = c.vs + pg * c.vsp;
+        const bool all = pg >= 0;
+        const long long row = (long long)r * c.psz + t0 % c.psz + first_row, page = all ? pg : 0;
+        uint8_t* kc = c.kc + page * c.kcp + row * (D / 2) + key_word<D>(sub) * 4;
+        uint8_t* vc = c.vc + page * c.vcp + row * (D / 2) + sub * 4;
+        uint8_t* ks = c.ks + page * c.ksp + row * (D / kGrp) + (sub >> 2);
+        uint8_t* vs = c.vs + page * c.vsp + row * (D / kGrp) + (sub >> 2);
         Sum run;
         run.init();
-        constexpr int U = 4, STEP = kBulkWarps * R::KPI;
-        for (int base = t0 + warp * R::KPI + grp; base - grp < t1; base += U * STEP) {
-            uint4 kr[U], vr[U];
+        for (; __any_sync(0xffffffffu, left > 0); left -= U * STEP) {
+            float k[U][8], z[U], top = run.m;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {   // rows past the end re-read the last one and are not used
-                const int t = min(base + u * STEP, t1 - 1) - L;
-                kr[u] = *reinterpret_cast<const uint4*>(kb + (long long)t * s.ks[1]);
-                vr[u] = *reinterpret_cast<const uint4*>(vb + (long long)t * s.vs[1]);
+            for (int u = 0; u < U; ++u) {
+                Vec<__nv_bfloat16>::cvt(kr[u], k[u]);
+                z[u] = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[u] = fmaf(qv[e], k[u][e], z[u]);
+#pragma unroll
+                for (int o = R::LPK / 2; o > 0; o >>= 1) z[u] += __shfl_xor_sync(0xffffffffu, z[u], o);
+                if (left <= u * STEP) z[u] = -INFINITY;
+                top = fmaxf(top, z[u]);
+            }
+            const float ref = top == -INFINITY ? 0.f : top, sc = exp2f(run.m - ref);
+            run.m = top;
+            run.l *= sc;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) run.a[e] *= sc;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float p = exp2f(z[u] - ref);   // 0 for rows that are not there (their keys are zeros)
+                run.l += p;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) run.a[e] = fmaf(p, k[u][e], run.a[e]);
+                uint32_t sb;
+                const uint32_t w = quant8(kr[u], k[u], ke, &sb);
+                if (all && left > u * STEP) {
+                    *reinterpret_cast<uint32_t*>(kc + u * STEP * (D / 2)) = w;
+                    if ((sub & 3) == 0) ks[u * STEP * (D / kGrp)] = (uint8_t)sb;
+                }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int t = base + u * STEP;
-                float k[8], z = 0.f;
-                Vec<__nv_bfloat16>::cvt(kr[u], k);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) z = fmaf(qv[e], k[e], z);
-#pragma unroll
-                for (int o = R::LPK / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-                uint32_t ksc, vsc;
-                const uint32_t kw = quant8(kr[u], ke, &ksc), vw = quant8(vr[u], ve, &vsc);
-                if (t < t1) {
-                    run.push(z, k);
-                    if (pg >= 0) {
-                        write_row<D>(kc, ks, row0 + t - t0, sub, key_word<D>(sub), kw, ksc);
-                        write_row<D>(vc, vs, row0 + t - t0, sub, sub, vw, vsc);
-                    }
+                float v[8];
+                Vec<__nv_bfloat16>::cvt(vr[u], v);
+                uint32_t sb;
+                const uint32_t w = quant8(vr[u], v, ve, &sb);
+                if (all && left > u * STEP) {
+                    *reinterpret_cast<uint32_t*>(vc + u * STEP * (D / 2)) = w;
+                    if ((sub & 3) == 0) vs[u * STEP * (D / kGrp)] = (uint8_t)sb;
                 }
             }
+            kc += U * STEP * (D / 2);
+            vc += U * STEP * (D / 2);
+            ks += U * STEP * (D / kGrp);
+            vs += U * STEP * (D / kGrp);
+            load(left - U * STEP);
         }
 #pragma unroll
         for (int o = R::LPK; o < 32; o <<= 1) {
@@ -280,7 +340,7 @@ __global__ void append_few_kernel(Shape s, Q4 c, Append a)
 #pragma unroll
             for (int o = R::LPK / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
             uint32_t sc;
-            const uint32_t w = quant8(raw, inv_e, &sc);
+            const uint32_t w = quant8(raw, k, inv_e, &sc);
             if (pg >= 0 && grp < 2) {
                 const long long row = (long long)r * c.psz + t % c.psz;
                 if (val) write_row<D>(c.vc + pg * c.vcp, c.vs + pg * c.vsp, row, sub, sub, w, sc);
@@ -314,7 +374,8 @@ constexpr int kLoadWarps = 8, kLoadRows = 4;
 
 __device__ __forceinline__ uint32_t bf2(uint32_t pair, __nv_bfloat162 s)
 {
-    uint32_t w = (pair & 0x000f000fu) | 0x43004300u;
+    uint32_t w;   // (pair & 0x000f000f) | 0x43004300 in one instruction
+    asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(w) : "r"(pair), "r"(0x43004300u));
     __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162*>(&w);
     v = __hmul2(__hsub2(v, __float2bfloat162_rn(136.f)), s);
     return *reinterpret_cast<uint32_t*>(&v);
@@ -329,22 +390,32 @@ __global__ void __launch_bounds__(32 * kLoadWarps) load_kernel(Shape s, Q4 c, Lo
     const long long first = (a.start ? (long long)a.start[b] : 0) + a.offset;
     const int len = min(a.seqlens[b], s.n);
     const int j0 = (blockIdx.x * kLoadWarps + warp) * R::KPI * kLoadRows + grp;
+    // the lane's tokens are KPI apart: together at most as far as a page is long, so one division will do
+    static_assert(R::KPI * kLoadRows <= 16, "pages hold at least 16 tokens");
+    const long long t0 = first + j0;
+    const int q0 = t0 >= 0 && t0 < len ? (int)t0 : 0, slot0 = q0 / c.psz, in0 = q0 - slot0 * c.psz;
+    const int* table = c.pt + (long long)b * c.pmax;
     uint32_t kw[kLoadRows], vw[kLoadRows], kq[kLoadRows], vq[kLoadRows];
 #pragma unroll
     for (int u = 0; u < kLoadRows; ++u) {
-        const int j = j0 + u * R::KPI;
-        const long long t = first + j;
         kw[u] = vw[u] = kq[u] = vq[u] = 0;   // scale 0: the value 0
-        if (j < a.n && t >= 0 && t < len) {
-            const int pg = q4_page(c, b, (int)t);
-            if (pg >= 0) {
-                const long long row = (long long)r * c.psz + (int)t % c.psz;
-                kw[u] = *reinterpret_cast<const uint32_t*>(c.kc + pg * c.kcp + row * (D / 2) + key_word<D>(sub) * 4);
-                vw[u] = *reinterpret_cast<const uint32_t*>(c.vc + pg * c.vcp + row * (D / 2) + sub * 4);
-                kq[u] = c.ks[pg * c.ksp + row * (D / kGrp) + (sub >> 2)];
-                vq[u] = c.vs[pg * c.vsp + row * (D / kGrp) + (sub >> 2)];
-            }
+        const long long t = t0 + u * R::KPI;
+        if (j0 + u * R::KPI >= a.n || t < 0 || t >= len) continue;
+        int slot = slot0, in = in0 + u * R::KPI;
+        if (t0 < 0) {   // the first token lies before the sequence
+            slot = (int)t / c.psz;
+            in = (int)t - slot * c.psz;
+        } else if (in >= c.psz) {
+            ++slot;
+            in -= c.psz;
         }
+        const int pg = slot < c.pmax ? __ldg(table + slot) : -1;
+        if (pg < 0 || pg >= c.npages) continue;
+        const long long row = (long long)r * c.psz + in;
+        kw[u] = *reinterpret_cast<const uint32_t*>(c.kc + pg * c.kcp + row * (D / 2) + key_word<D>(sub) * 4);
+        vw[u] = *reinterpret_cast<const uint32_t*>(c.vc + pg * c.vcp + row * (D / 2) + sub * 4);
+        kq[u] = c.ks[pg * c.ksp + row * (D / kGrp) + (sub >> 2)];
+        vq[u] = c.vs[pg * c.vsp + row * (D / kGrp) + (sub >> 2)];
     }
     const float ke = exp2i(c.kexp), ve = exp2i(c.vexp);
     auto put = [&](__nv_bfloat16* out, uint32_t w, uint32_t sb, float e) {
@@ -359,12 +430,15 @@ __global__ void __launch_bounds__(32 * kLoadWarps) load_kernel(Shape s, Q4 c, Lo
         o.w = __byte_perm(p[2], p[3], 0x7632);
         *reinterpret_cast<uint4*>(out) = o;
     };
+    __nv_bfloat16* ko = a.K + (long long)b * s.ks[0] + (long long)j0 * s.ks[1] + (long long)r * s.ks[2] + sub * 8;
+    __nv_bfloat16* vo = a.V + (long long)b * s.vs[0] + (long long)j0 * s.vs[1] + (long long)r * s.vs[2] + sub * 8;
 #pragma unroll
     for (int u = 0; u < kLoadRows; ++u) {
-        const int j = j0 + u * R::KPI;
-        if (j >= a.n) continue;
-        put(a.K + (long long)b * s.ks[0] + (long long)j * s.ks[1] + (long long)r * s.ks[2] + sub * 8, kw[u], kq[u], ke);
-        put(a.V + (long long)b * s.vs[0] + (long long)j * s.vs[1] + (long long)r * s.vs[2] + sub * 8, vw[u], vq[u], ve);
+        if (j0 + u * R::KPI >= a.n) break;
+        put(ko, kw[u], kq[u], ke);
+        put(vo, vw[u], vq[u], ve);
+        ko += R::KPI * s.ks[1];
+        vo += R::KPI * s.vs[1];
     }
 }
 
