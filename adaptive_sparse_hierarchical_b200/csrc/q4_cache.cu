@@ -30,31 +30,33 @@ struct Row {
     static constexpr int LPK = D / 8, KPI = 32 / LPK;
 };
 
-// Codes of the 8 elements x of this lane (raw: their bf16 bits) and its group's scale byte (equal in the
-// group's 4 lanes).  inv_e = 2^-e.  Every lane of the warp takes part.
-__device__ __forceinline__ uint32_t quant8(uint4 raw, const float* x, float inv_e, uint32_t* scale)
+// Scale byte of a group from its largest |x| (two bf16 bit patterns, either may be it), the factor 2^-e / s
+// of its elements (inv_e = 2^-e; 0 where s is 0), and whether its quotients may have to be clamped (a
+// subnormal or the largest scale).
+__device__ __forceinline__ float group_scale(uint32_t top2, float inv_e, uint32_t* scale, bool* edge)
 {
-    // |x| as bf16 bits: ordered as integers, infinities and NaNs on top
-    uint32_t t = __vmaxu2(__vmaxu2(raw.x & 0x7fff7fffu, raw.y & 0x7fff7fffu),
-                          __vmaxu2(raw.z & 0x7fff7fffu, raw.w & 0x7fff7fffu));
-    t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, 1));
-    t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, 2));
-    const uint32_t top = max(t << 16, t & 0xffff0000u);   // as fp32 bits
+    const uint32_t top = max(top2 << 16, top2 & 0xffff0000u);   // as fp32 bits
     const float f = top < 0x7f800000u ? __uint_as_float(top) * inv_e * (1.f / 7.f) : __int_as_float(0x7fffffff);
     uint32_t sb, h;
-    float s, r;
+    float r;
     asm("{\n\t.reg .b16 b;\n\tcvt.rn.f16x2.f32 %1, %2, %2;\n\tcvt.rn.satfinite.e4m3x2.f16x2 b, %1;\n\t"
         "cvt.u32.u16 %0, b;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}\n"
         : "=r"(sb), "=r"(h)
         : "f"(f));
-    s = __half2float(__ushort_as_half((unsigned short)h));
+    const float s = __half2float(__ushort_as_half((unsigned short)h));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-    r = s == 0.f ? 0.f : r * inv_e;
-    *scale = sb = sb & 0xffu;
+    *scale = sb & 0xffu;
+    *edge = (sb & 0xffu) - 1u < 7u || (sb & 0xffu) == 0x7eu;
+    return s == 0.f ? 0.f : r * inv_e;
+}
+
+// The word of codes of 8 elements (r: group_scale's factor; clamp: whether any quotient may need it).
+__device__ __forceinline__ uint32_t codes8(const float* x, float r, bool clamp)
+{
     __half2 y[4];   // elements i and i + 4
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = __floats2half2_rn(x[i] * r, x[i + 4] * r);
-    if (__any_sync(0xffffffffu, sb - 1u < 7u || sb == 0x7eu)) {   // a subnormal or the largest scale in the warp
+    if (clamp) {
         const __half2 lo = __float2half2_rn(-7.f), hi = __float2half2_rn(7.f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = __hmin2(__hmax2(y[i], lo), hi);
@@ -66,6 +68,20 @@ __device__ __forceinline__ uint32_t quant8(uint4 raw, const float* x, float inv_
         w += *reinterpret_cast<const uint32_t*>(&u) << (4 * i);
     }
     return w;
+}
+
+// Codes of the 8 elements x of this lane (raw: their bf16 bits) and its group's scale byte (equal in the
+// group's 4 lanes).  Every lane of the warp takes part.
+__device__ __forceinline__ uint32_t quant8(uint4 raw, const float* x, float inv_e, uint32_t* scale)
+{
+    // |x| as bf16 bits: ordered as integers, infinities and NaNs on top
+    uint32_t t = __vmaxu2(__vmaxu2(raw.x & 0x7fff7fffu, raw.y & 0x7fff7fffu),
+                          __vmaxu2(raw.z & 0x7fff7fffu, raw.w & 0x7fff7fffu));
+    t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, 1));
+    t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, 2));
+    bool edge;
+    const float r = group_scale(t, inv_e, scale, &edge);
+    return codes8(x, r, __any_sync(0xffffffffu, edge));
 }
 
 // Place of a key row's word `sub` (elements 8 sub ..): word j = sub % 4 of group sub / 4.
@@ -88,16 +104,6 @@ struct Sum {
         l = fmaf(l, sc, p);
 #pragma unroll
         for (int e = 0; e < 8; ++e) a[e] = fmaf(a[e], sc, p * k[e]);
-        m = mn;
-    }
-    __device__ void merge(float m2, float l2, const float* a2)
-    {
-        const float mn = fmaxf(m, m2);
-        if (mn == -INFINITY) return;
-        const float s1 = exp2f(m - mn), s2 = exp2f(m2 - mn);
-        l = l * s1 + l2 * s2;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] = a[e] * s1 + a2[e] * s2;
         m = mn;
     }
 };
@@ -143,149 +149,202 @@ __device__ __forceinline__ void write_summary(float* out, int sub, const Sum& r)
     for (int e = 0; e < 8; ++e) out[sub * 8 + e] = r.a[e] * inv;
 }
 
-// One block of four warps per (touched chunk, KV head, sequence): the chunk's new keys and values
-// are quantised and its keys summarised in one pass; the warps' sums merge in order.  The block of
-// the first chunk also takes the chunk left open at the end, so that the state is read and written
-// by one block, in that order.
+// Many tokens: a warp per (touched chunk, KV head, sequence) quantises the chunk's new keys and sums them
+// up in one pass, another one the values.  Four lanes share a row: lane q holds the q-th quarter of every
+// scale group.  The groups' maxima are reduced so that each lane is left with one group, whose scale it
+// computes for all four (the scale is a third of the work when every lane does it); loads stay 64 bytes
+// contiguous and a key's words come out in storage order.  The eight rows' sums of a warp are added by a
+// reduce-scatter.  2 x 65536 tokens x 2 heads x 128 (134 MB in, 36 MB out): 41 us,
+// 4.1 TB/s; with 8 elements and a scale per lane 50 us.
+// The warp of the first chunk also takes the chunk left open at the end, so that the state is read and
+// written by one warp, in that order.
+template <int NG>
+struct RowQuant {
+    uint32_t word[NG];
+    uint32_t scale;   // byte of the group that this lane owns: q for 4 groups, q / 2 for 2
+
+    __device__ __forceinline__ void operator()(const uint4* raw, const float (*x)[8], float inv_e)
+    {
+        const int q = threadIdx.x & 3;
+        // |x| as bf16 bits, two at a time: ordered as integers, infinities and NaNs on top
+        uint32_t t[NG];
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+            t[i] = __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
+                            __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu));
+        uint32_t own;
+        if constexpr (NG == 4) {
+            const bool b1 = q & 2, b0 = q & 1;
+            uint32_t k0 = b1 ? t[2] : t[0], k1 = b1 ? t[3] : t[1];
+            k0 = __vmaxu2(k0, __shfl_xor_sync(0xffffffffu, b1 ? t[0] : t[2], 2));
+            k1 = __vmaxu2(k1, __shfl_xor_sync(0xffffffffu, b1 ? t[1] : t[3], 2));
+            own = __vmaxu2(b0 ? k1 : k0, __shfl_xor_sync(0xffffffffu, b0 ? k0 : k1, 1));
+        } else {
+            const bool b1 = q & 2;
+            own = __vmaxu2(b1 ? t[1] : t[0], __shfl_xor_sync(0xffffffffu, b1 ? t[0] : t[1], 2));
+            own = __vmaxu2(own, __shfl_xor_sync(0xffffffffu, own, 1));
+        }
+        bool edge;
+        const float r = group_scale(own, inv_e, &scale, &edge);
+        edge = __any_sync(0xffffffffu, edge);
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+            word[i] = codes8(x[i], __shfl_sync(0xffffffffu, r, (threadIdx.x & 28) | (NG == 4 ? i : 2 * i)), edge);
+    }
+};
+
 template <int D>
 __global__ void __launch_bounds__(32 * kBulkWarps, 4)
-append_bulk_kernel(Shape s, Q4 c, Append a)
+append_bulk_kernel(Shape s, Q4 c, Append a, int chunks, long long warps)
 {
-    using R = Row<D>;
+    constexpr int NG = D / kGrp, N = NG * 8;   // elements of a row per lane: group i, elements 8 q .. 8 q + 7
+    pdl_wait();
     pdl_launch_dependents();
-    __shared__ float part[kBulkWarps][D + 2];
-    const int b = blockIdx.z, r = blockIdx.y;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane / R::LPK, sub = lane % R::LPK;
+    __shared__ __align__(16) float qsm[kBulkWarps][D];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, slot = lane >> 2;
+    const long long wid = (long long)blockIdx.x * kBulkWarps + warp;
+    if (wid >= warps) return;
+    const int chunk_i = (int)(wid % chunks), rest = (int)(wid / chunks);
+    const bool val = rest & 1;
+    const int r = (rest >> 1) % s.hkv, b = (rest >> 1) / s.hkv;
     int L, n;
     span(s, a, b, &L, &n);
     if (n == 0) return;
-    const int end = L + n, first = L / s.B, ci = first + blockIdx.x, open = end / s.B;
-    if (ci * s.B >= end || (ci == open && ci != first)) return;
-    float qv[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) qv[e] = a.qbar[r * D + sub * 8 + e] * (kLog2e * rsqrtf((float)D));
-    const float ke = exp2i(-c.kexp), ve = exp2i(-c.vexp);
+    const int end = L + n, first = L / s.B, ci = first + chunk_i, open = end / s.B;
+    if ((long long)ci * s.B >= end || (ci == open && ci != first)) return;
+    const float inv_e = exp2i(val ? -c.vexp : -c.kexp);
+    const long long ld = val ? s.vs[1] : s.ks[1];
+    const __nv_bfloat16* src = (val ? a.V + (long long)b * s.vs[0] + (long long)r * s.vs[2]
+                                    : a.K + (long long)b * s.ks[0] + (long long)r * s.ks[2]) + q * 8;
     float* st = a.state + ((long long)b * s.hkv + r) * (D + 2);
-    const __nv_bfloat16* kb = a.K + (long long)b * s.ks[0] + (long long)r * s.ks[2] + sub * 8;
-    const __nv_bfloat16* vb = a.V + (long long)b * s.vs[0] + (long long)r * s.vs[2] + sub * 8;
+    const float* qrow = qsm[warp];
+    if (!val) {
+        for (int d = lane; d < D; d += 32) qsm[warp][d] = a.qbar[r * D + d] * (kLog2e * rsqrtf((float)D));
+        __syncwarp();
+    }
 
     auto chunk = [&](int cc, bool with_state) {
-        const int t0 = max(cc * s.B, L), t1 = min((cc + 1) * s.B, end);
-        // This lane's rows are first_row + i STEP of the chunk; the first ones are on their way before the page
-        // is known, the next ones before the present ones are worked on.
-        constexpr int U = 4, STEP = kBulkWarps * R::KPI;
-        const int first_row = warp * R::KPI + grp;
-        const __nv_bfloat16* kp = kb + (long long)(t0 - L + first_row) * s.ks[1];
-        const __nv_bfloat16* vp = vb + (long long)(t0 - L + first_row) * s.vs[1];
-        const long long kstep = STEP * s.ks[1], vstep = STEP * s.vs[1];
-        int left = t1 - t0 - first_row;   // row i is there while left > i STEP
-        uint4 kr[U], vr[U];
-        auto load = [&](int rows) {
+        const int t0 = max(cc * s.B, L), len = min((cc + 1) * s.B, end) - t0;
+        const __nv_bfloat16* p = src + (long long)(t0 - L + slot) * ld;
+        uint4 nx[NG];
+        auto load = [&](int row) {   // the rows after the last one read as zeros
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                kr[u] = vr[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (rows > u * STEP) {
-                    kr[u] = *reinterpret_cast<const uint4*>(kp);
-                    vr[u] = *reinterpret_cast<const uint4*>(vp);
-                }
-                kp += kstep;
-                vp += vstep;
+            for (int i = 0; i < NG; ++i) {
+                nx[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (row < len) nx[i] = __ldcs(reinterpret_cast<const uint4*>(p + i * kGrp));
             }
+            p += 8 * ld;
         };
-        load(left);
+        load(slot);   // on its way before the page is known
         const int pg = q4_page(c, b, t0);
-        const bool all = pg >= 0;
-        const long long row = (long long)r * c.psz + t0 % c.psz + first_row, page = all ? pg : 0;
-        uint8_t* kc = c.kc + page * c.kcp + row * (D / 2) + key_word<D>(sub) * 4;
-        uint8_t* vc = c.vc + page * c.vcp + row * (D / 2) + sub * 4;
-        uint8_t* ks = c.ks + page * c.ksp + row * (D / kGrp) + (sub >> 2);
-        uint8_t* vs = c.vs + page * c.vsp + row * (D / kGrp) + (sub >> 2);
-        Sum run;
-        run.init();
-        for (; __any_sync(0xffffffffu, left > 0); left -= U * STEP) {
-            float k[U][8], z[U], top = run.m;
+        const long long page = pg >= 0 ? pg : 0, row0 = (long long)r * c.psz + t0 % c.psz + slot;
+        uint8_t* codes = (val ? c.vc + page * c.vcp : c.kc + page * c.kcp) + row0 * (D / 2);
+        uint8_t* scales = (val ? c.vs + page * c.vsp : c.ks + page * c.ksp) + row0 * NG;
+        // sums of this lane's elements over its slot's rows, relative to ref (which follows the maximum m of
+        // the logits at a distance of 8 at most)
+        float m = -INFINITY, ref = -INFINITY, l = 0.f, acc[N];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                Vec<__nv_bfloat16>::cvt(kr[u], k[u]);
-                z[u] = 0.f;
+        for (int e = 0; e < N; ++e) acc[e] = 0.f;
+        for (int row = slot; row - slot < len; row += 8) {
+            uint4 raw[NG];
+            float x[NG][8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) z[u] = fmaf(qv[e], k[u][e], z[u]);
-#pragma unroll
-                for (int o = R::LPK / 2; o > 0; o >>= 1) z[u] += __shfl_xor_sync(0xffffffffu, z[u], o);
-                if (left <= u * STEP) z[u] = -INFINITY;
-                top = fmaxf(top, z[u]);
+            for (int i = 0; i < NG; ++i) {
+                raw[i] = nx[i];
+                Vec<__nv_bfloat16>::cvt(raw[i], x[i]);
             }
-            const float ref = top == -INFINITY ? 0.f : top, sc = exp2f(run.m - ref);
-            run.m = top;
-            run.l *= sc;
+            load(row + 8);
+            if (!val) {
+                float z = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) run.a[e] *= sc;
+                for (int i = 0; i < NG; ++i)
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const float p = exp2f(z[u] - ref);   // 0 for rows that are not there (their keys are zeros)
-                run.l += p;
+                    for (int e = 0; e < 8; e += 4) {
+                        const float4 w = *reinterpret_cast<const float4*>(qrow + i * kGrp + q * 8 + e);
+                        z = fmaf(w.x, x[i][e], fmaf(w.y, x[i][e + 1], fmaf(w.z, x[i][e + 2], fmaf(w.w, x[i][e + 3], z))));
+                    }
+                z += __shfl_xor_sync(0xffffffffu, z, 1);
+                z += __shfl_xor_sync(0xffffffffu, z, 2);
+                if (row >= len) z = -INFINITY;
+                m = fmaxf(m, z);
+                if (__any_sync(0xffffffffu, z > ref + 8.f)) {
+                    const float to = z > ref + 8.f ? z : ref, f = to == -INFINITY ? 1.f : exp2f(ref - to);
+                    ref = to;
+                    l *= f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) run.a[e] = fmaf(p, k[u][e], run.a[e]);
-                uint32_t sb;
-                const uint32_t w = quant8(kr[u], k[u], ke, &sb);
-                if (all && left > u * STEP) {
-                    *reinterpret_cast<uint32_t*>(kc + u * STEP * (D / 2)) = w;
-                    if ((sub & 3) == 0) ks[u * STEP * (D / kGrp)] = (uint8_t)sb;
+                    for (int e = 0; e < N; ++e) acc[e] *= f;
                 }
-            }
+                const float w = exp2f(z - (ref == -INFINITY ? 0.f : ref));   // 0 for rows that are not there
+                l += w;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float v[8];
-                Vec<__nv_bfloat16>::cvt(vr[u], v);
-                uint32_t sb;
-                const uint32_t w = quant8(vr[u], v, ve, &sb);
-                if (all && left > u * STEP) {
-                    *reinterpret_cast<uint32_t*>(vc + u * STEP * (D / 2)) = w;
-                    if ((sub & 3) == 0) vs[u * STEP * (D / kGrp)] = (uint8_t)sb;
+                for (int e = 0; e < N; ++e) acc[e] = fmaf(w, x[e >> 3][e & 7], acc[e]);
+            }
+            RowQuant<NG> out;
+            out(raw, x, inv_e);
+            if (row < len && pg >= 0) {
+                if (val) {
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) *reinterpret_cast<uint32_t*>(codes + (4 * i + q) * 4) = out.word[i];
+                } else if constexpr (NG == 4) {
+                    *reinterpret_cast<uint4*>(codes + q * 16) = make_uint4(out.word[0], out.word[1], out.word[2], out.word[3]);
+                } else {
+                    *reinterpret_cast<uint2*>(codes + q * 8) = make_uint2(out.word[0], out.word[1]);
                 }
+                if (NG == 4 || !(q & 1)) scales[NG == 4 ? q : q >> 1] = (uint8_t)out.scale;
             }
-            kc += U * STEP * (D / 2);
-            vc += U * STEP * (D / 2);
-            ks += U * STEP * (D / kGrp);
-            vs += U * STEP * (D / kGrp);
-            load(left - U * STEP);
+            codes += 8 * (D / 2);
+            scales += 8 * NG;
         }
+        if (val) return;
+        // one reference for the warp (and the state it continues), then the sums
+        float M = m;
 #pragma unroll
-        for (int o = R::LPK; o < 32; o <<= 1) {
-            const float m2 = __shfl_xor_sync(0xffffffffu, run.m, o), l2 = __shfl_xor_sync(0xffffffffu, run.l, o);
-            float a2[8];
+        for (int o = 4; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float m0 = with_state ? st[D] : -INFINITY;
+        M = fmaxf(M, m0);
+        const float base = M == -INFINITY ? 0.f : M;
+        // a slot without a reference holds zeros, or NaNs that have to stay
+        const float f = ref == -INFINITY ? 1.f : exp2f(ref - base), f0 = m0 == -INFINITY ? 0.f : exp2f(m0 - base);
+        l *= f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) a2[e] = __shfl_xor_sync(0xffffffffu, run.a[e], o);
-            run.merge(m2, l2, a2);
+        for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[e] *= f;
+#pragma unroll
+        for (int h = N / 2; h >= NG; h >>= 1) {   // halves go to lanes 16, 8 and 4 apart
+            const int o = 16 * h / (N / 2);
+            const bool up = lane & o;
+#pragma unroll
+            for (int e = 0; e < h; ++e)
+                acc[e] = (up ? acc[e + h] : acc[e]) + __shfl_xor_sync(0xffffffffu, up ? acc[e] : acc[e + h], o);
         }
-        if (grp == 0) write_state<D>(part[warp], sub, run);
-        __syncthreads();
-        if (warp == 0 && grp == 0) {
-            for (int w = 1; w < kBulkWarps; ++w) run.merge(part[w][D], part[w][D + 1], part[w] + sub * 8);
-            if (with_state) {
-                float old[8];
+        // lane bits 4, 3, 2 number the piece of NG elements that is left
+        const int piece = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1), e0 = piece * NG;
+        const int d0 = (e0 >> 3) * kGrp + q * 8 + (e0 & 7);
+        if (with_state) {
+            l = fmaf(st[D + 1], f0, l);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) old[e] = st[sub * 8 + e];
-                run.merge(st[D], st[D + 1], old);
-            }
-            __syncwarp((1ull << R::LPK) - 1);   // the state is read by these lanes before it is written
-            if ((cc + 1) * s.B <= end)
-                write_summary<D>(a.kbar + (((long long)b * s.hkv + r) * s.T + cc) * D, sub, run);
-            else
-                write_state<D>(st, sub, run);
+            for (int e = 0; e < NG; ++e) acc[e] = fmaf(st[d0 + e], f0, acc[e]);
+            __syncwarp();   // the state is read before it is written
         }
-        __syncthreads();   // `part` is used again
+        if ((cc + 1) * s.B <= end) {
+            float* out = a.kbar + (((long long)b * s.hkv + r) * s.T + cc) * D + d0;
+            const float inv = 1.f / l;
+#pragma unroll
+            for (int e = 0; e < NG; ++e) out[e] = acc[e] * inv;
+        } else {
+#pragma unroll
+            for (int e = 0; e < NG; ++e) st[d0 + e] = acc[e];
+            if (lane == 0) { st[D] = M; st[D + 1] = l; }
+        }
     };
     chunk(ci, ci == first && L % s.B != 0);
-    if (blockIdx.x == 0) {
-        if (end % s.B == 0) {
-            if (warp == 0 && grp == 0) {
-                Sum none;
-                none.init();
-                write_state<D>(st, sub, none);
-            }
-        } else if (open != first) {
-            chunk(open, false);
+    if (chunk_i == 0) {
+        if (end % s.B != 0) {
+            if (open != first) chunk(open, false);
+        } else if (!val) {
+            __syncwarp();
+            for (int d = lane; d < D + 2; d += 32) st[d] = d == D ? -INFINITY : 0.f;
         }
     }
 }
@@ -308,6 +367,7 @@ template <int D>
 __global__ void append_few_kernel(Shape s, Q4 c, Append a)
 {
     using R = Row<D>;
+    pdl_wait();
     pdl_launch_dependents();   // the decode routing that follows waits for this grid itself
     const int b = blockIdx.x, lane = threadIdx.x & 31, grp = lane / R::LPK, sub = lane % R::LPK;
     int L, n;
@@ -385,6 +445,8 @@ template <int D>
 __global__ void __launch_bounds__(32 * kLoadWarps) load_kernel(Shape s, Q4 c, Load a)
 {
     using R = Row<D>;
+    pdl_wait();
+    pdl_launch_dependents();
     const int b = blockIdx.z, r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int grp = lane / R::LPK, sub = lane % R::LPK;
     const long long first = (a.start ? (long long)a.start[b] : 0) + a.offset;
@@ -447,13 +509,12 @@ cudaError_t append_d(const Shape& s, const Q4& c, const Append& a, cudaStream_t 
 {
     // Up to this many tokens a warp walks them one after another (about 1 us each) and saves the
     // second launch.
-    if (a.n_new <= 4) {
-        append_few_kernel<D><<<s.batch, 32 * (s.hkv < 16 ? s.hkv : 16), 0, st>>>(s, c, a);
-        return cudaGetLastError();
-    }
+    if (a.n_new <= 4)
+        return launch_after(append_few_kernel<D>, dim3(s.batch), dim3(32 * (s.hkv < 16 ? s.hkv : 16)), 0, st, s, c, a);
     const int chunks = (a.n_new + s.B - 2) / s.B + 1;
-    append_bulk_kernel<D><<<dim3(chunks, s.hkv, s.batch), 32 * kBulkWarps, 0, st>>>(s, c, a);
-    cudaError_t e = cudaGetLastError();
+    const long long warps = 2ll * chunks * s.hkv * s.batch;
+    const cudaError_t e = launch_after(append_bulk_kernel<D>, dim3((unsigned)((warps + kBulkWarps - 1) / kBulkWarps)),
+                                       dim3(32 * kBulkWarps), 0, st, s, c, a, chunks, warps);
     if (e != cudaSuccess) return e;
     return launch_after(append_len_kernel, dim3(1), dim3(s.batch < 256 ? (s.batch + 31) / 32 * 32 : 256), 0, st, s, a);
 }
@@ -473,9 +534,7 @@ cudaError_t launch_load_q4(const Shape& s, const Q4& c, const int* start, int of
     const Load a{(__nv_bfloat16*)K, (__nv_bfloat16*)V, start, seqlens, offset, n};
     const int per = kLoadWarps * kLoadRows * (256 / s.d);
     const dim3 grid((unsigned)(((long long)n + per - 1) / per), s.hkv, s.batch);
-    if (s.d == 128) load_kernel<128><<<grid, 32 * kLoadWarps, 0, st>>>(s, c, a);
-    else load_kernel<64><<<grid, 32 * kLoadWarps, 0, st>>>(s, c, a);
-    return cudaGetLastError();
+    return launch_after(s.d == 128 ? load_kernel<128> : load_kernel<64>, grid, dim3(32 * kLoadWarps), 0, st, s, c, a);
 }
 
 }  // namespace dash
