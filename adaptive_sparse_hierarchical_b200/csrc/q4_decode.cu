@@ -40,9 +40,7 @@ namespace dash {
 namespace {
 
 constexpr int kMaxPairs = 2048;
-constexpr int kMaxBlocks = 1024;
-// Granules that a second pair costs a block, in time: about 5 us against 2.4 us per round of its warps.
-constexpr int kTurn = 32;
+constexpr int kMaxBlocks = 2048;
 constexpr int kMeta = 64;         // granule descriptors per warp (two halves of 32)
 
 // Descriptor of a granule: where its codes and scales lie, its chunk's bias, tokens | mapped << 8.
@@ -52,8 +50,9 @@ struct Meta {
     int nv[kMeta];
 };
 
-// Warps per block: one block per SM, as many warps as the registers of NT head tiles allow.
-template <int NT> struct Cfg { static constexpr int W = NT == 1 ? 16 : 12; };
+// Eight warps per block and as many blocks per SM as the registers of NT head tiles allow: two blocks merge
+// and start at different times, and the tensor and integer pipes need no more warps than that.
+template <int NT> struct Cfg { static constexpr int W = 8, BLOCKS = NT == 1 ? 2 : 1; };
 
 // Granules of 16 U tokens (U = 2 wherever the chunk allows: descriptors, waits and votes are paid once for
 // twice the tokens, and the warp has two independent chains to issue from); the ring holds 64 tokens.
@@ -125,14 +124,14 @@ __device__ __forceinline__ int tok_of(int m) { return (m & 1) ? ((m >> 1) ^ 1) +
 __device__ __forceinline__ int len_of(const Shape& s, const int* seqlens, int b) { return min(max(seqlens[b], 0), s.n); }
 
 template <int D, int NT, int U>
-__global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, Q4 c, Routes rt, Attend a)
+__global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_kernel(Shape s, Q4 c, Routes rt, Attend a)
 {
     constexpr int W = Cfg<NT>::W, NG = D / kGrp, NW = D / 64, MT = D / 16;
     using St = Stage<D, U>;
     constexpr int OLD = St::OLD, kGran = St::GRAN, kStages = St::N;
     static_assert(8 * NT * OLD * 4 <= kStages * St::BYTES, "the merge buffer reuses a warp's ring");
     extern __shared__ __align__(128) char smem[];
-    __shared__ int pre[kMaxPairs + 1], first_blk[kMaxBlocks + 1], own_blocks;
+    __shared__ int pre[kMaxPairs + 1], first_blk[kMaxBlocks + 1], range[3];
     __shared__ float mrg_m[W][8 * NT], mrg_l[W][8 * NT], mrg_s[W][8 * NT], tot_m[8 * NT], tot_l[8 * NT];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -144,87 +143,64 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, 1) q4_attend_kernel(Shape s, 
         const int full = L > 0 ? (a.dense ? (L - 1) / s.B : rt.counts[x]) : 0;
         pre[x + 1] = L > 0 ? full * NB + ((L - 1) % s.B) / kGran + 1 : 0;
     }
-    if (threadIdx.x == 0) pre[0] = 0;
     __syncthreads();
     if (warp == 0) {
-        int run = 0;
-        for (int x0 = 0; x0 < BR; x0 += 32) {
-            int v = x0 + lane < BR ? pre[x0 + lane + 1] : 0;
+        auto scan = [&](int* v, auto f) {   // v[x + 1] = f(0) + .. + f(x), v[0] = 0; returns the sum
+            int run = 0;
+            for (int x0 = 0; x0 < BR; x0 += 32) {
+                const int x = x0 + lane;
+                int n = x < BR ? f(x) : 0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += u;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int u = __shfl_up_sync(0xffffffffu, n, o);
+                    if (lane >= o) n += u;
+                }
+                if (x < BR) v[x + 1] = run + n;
+                run += __shfl_sync(0xffffffffu, n, 31);
             }
-            if (x0 + lane < BR) pre[x0 + lane + 1] = run + v;
-            run += __shfl_sync(0xffffffffu, v, 31);
+            if (lane == 0) v[0] = 0;
+            __syncwarp();
+            return run;
+        };
+        auto last_le = [&](const int* v, int k) {   // the x with v[x] <= k < v[x + 1]
+            int l = 0, h = BR;
+            while (l < h) {
+                const int m = (l + h) >> 1;
+                if (v[m + 1] <= k) l = m + 1;
+                else h = m;
+            }
+            return l;
+        };
+        const int total = scan(pre, [&](int x) { return pre[x + 1]; }), nb = (int)gridDim.x;
+        // every warp of a block in use has a granule
+        int used = min(nb, (total + W - 1) / W), x = 0;
+        long long lo = (long long)total * blockIdx.x / max(used, 1), hi = (long long)total * (blockIdx.x + 1) / max(used, 1);
+        // Where one round of a block's warps is enough, pairs get blocks of their own: a pair that starts
+        // inside a block costs it a merge, a descriptor chase and an empty ring (three short sequences: 17.4
+        // us so, 18.9 with even shares; with more rounds even shares are as good or better).
+        if (BR <= nb && total <= nb * W && scan(first_blk, [&](int x) { return (pre[x + 1] - pre[x] + W - 1) / W; }) <= nb) {
+            used = first_blk[BR];
+            if ((int)blockIdx.x < used) {
+                x = last_le(first_blk, blockIdx.x);
+                lo = pre[x] + ((int)blockIdx.x - first_blk[x]) * W;
+                hi = min((int)lo + W, pre[x + 1]);
+            }
+        } else if ((int)blockIdx.x < used) {
+            x = last_le(pre, (int)lo);
+        }
+        if (lane == 0) {
+            range[0] = (int)lo;
+            range[1] = (int)blockIdx.x < used ? (int)hi : 0;
+            range[2] = x;
         }
     }
     __syncthreads();
-    const long long total = pre[BR];
-    // every warp of a block in use has a granule
-    int used = (int)min((long long)gridDim.x, (total + W - 1) / W);
-    // Blocks of their own for every pair, if that costs no block more than kTurn granules over an even
-    // share: a second pair in a block costs a merge, a descriptor chase and an empty ring.
-    if (warp == 0) {
-        int cap = 0;
-        if (BR <= used && total > 2ll * W * used) {   // (not for a round or two per warp)
-            auto blocks = [&](int m) {   // blocks needed when none takes more than m granules
-                int n = 0;
-                for (int x = lane; x < BR; x += 32) n += (pre[x + 1] - pre[x] + m - 1) / m;
-                return warp_isum(n);
-            };
-            int lo_c = (int)((total + used - 1) / used), hi_c = lo_c + kTurn;
-            if (blocks(hi_c) <= used) {
-                while (lo_c < hi_c) {
-                    const int m = (lo_c + hi_c) >> 1;
-                    if (blocks(m) <= used) hi_c = m;
-                    else lo_c = m + 1;
-                }
-                cap = hi_c;
-                int run = 0;
-                for (int x0 = 0; x0 < BR; x0 += 32) {
-                    const int x = x0 + lane;
-                    int v = x < BR ? (pre[x + 1] - pre[x] + cap - 1) / cap : 0;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int u = __shfl_up_sync(0xffffffffu, v, o);
-                        if (lane >= o) v += u;
-                    }
-                    if (x < BR) first_blk[x + 1] = run + v;
-                    run += __shfl_sync(0xffffffffu, v, 31);
-                }
-                if (lane == 0) first_blk[0] = 0;
-            }
-        }
-        if (lane == 0) own_blocks = cap > 0;
-    }
-    __syncthreads();
-    int lo, hi, x = 0;
-    auto last_le = [&](const int* v, int k) {   // the x with v[x] <= k < v[x + 1]
-        int l = 0, h = BR;
-        while (l < h) {
-            const int m = (l + h) >> 1;
-            if (v[m + 1] <= k) l = m + 1;
-            else h = m;
-        }
-        return l;
-    };
-    if (own_blocks) used = first_blk[BR];
     if (blockIdx.x == 0)
         for (int x = threadIdx.x; x < BR; x += 32 * W)
             if (pre[x] == pre[x + 1]) a.span[x] = make_int2(0, -1);
-    if ((int)blockIdx.x >= used) return;
-    if (own_blocks) {
-        x = last_le(first_blk, blockIdx.x);
-        const int k = first_blk[x + 1] - first_blk[x], j = blockIdx.x - first_blk[x];
-        const long long n = pre[x + 1] - pre[x];
-        lo = pre[x] + (int)(n * j / k);
-        hi = pre[x] + (int)(n * (j + 1) / k);
-    } else {
-        lo = (int)(total * blockIdx.x / used);
-        hi = (int)(total * (blockIdx.x + 1) / used);
-        x = last_le(pre, lo);
-    }
+    const int lo = range[0], hi = range[1];
+    if (hi == 0) return;   // a block without work
+    int x = range[2];
 
     char* ring = smem + warp * (kStages * St::BYTES);
     const uint32_t ring_a = smem_u32(ring);
@@ -708,7 +684,7 @@ cudaError_t attend_t(const Shape& s, const Q4& c, const Routes& rt, const Attend
     const size_t smem = (size_t)Cfg<NT>::W * (Stage<D, U>::N * Stage<D, U>::BYTES + sizeof(Meta));
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    e = launch_after(k, dim3(dec_tma_blocks()), dim3(32 * Cfg<NT>::W), smem, st, s, c, rt, a);
+    e = launch_after(k, dim3(Cfg<NT>::BLOCKS * dec_tma_blocks()), dim3(32 * Cfg<NT>::W), smem, st, s, c, rt, a);
     if (e != cudaSuccess) return e;
     const int pairs = s.batch * s.hkv;
     return launch_after(q4_merge_kernel<D>, dim3(pairs, pairs * s.g <= 1024 ? s.g : 1), dim3(D * kMergeY), 0, st, s, a, c.vexp);
@@ -725,7 +701,7 @@ cudaError_t attend_d(const Shape& s, const Q4& c, const Routes& rt, const Attend
 
 int q4_max_pairs() { return kMaxPairs; }
 
-size_t q4_part_floats(const Shape& s) { return (size_t)dec_tma_blocks() * 2 * s.g * (s.d + 2); }
+size_t q4_part_floats(const Shape& s) { return (size_t)2 * dec_tma_blocks() * 2 * s.g * (s.d + 2); }
 
 cudaError_t launch_attend_q4(const Shape& s, const Q4& c, const void* q, const int* seqlens, const Routes& rt, bool dense,
                              float* part, int* span, void* O, cudaStream_t st)
