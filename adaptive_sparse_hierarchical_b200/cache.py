@@ -259,7 +259,9 @@ class PagePool:
         for t in pools:
             self.add_pages(t)
         self.add_rows(state.kbar, unit_tokens=state.p.chunk)
-        self.add_rows(state.state)
+        s = state.state
+        self._register(s, self._rows, L.dash_row_array(s.data_ptr(), s.stride(0) * 4, s.stride(1) * 4, s.shape[2] * 4,
+                                                       s.shape[1], 1, 0, L.DASH_ROW_STATE))
         if state.seqlens.data_ptr() != self.seqlens.data_ptr():
             self.add_rows(state.seqlens, clear=True)
 
@@ -273,10 +275,10 @@ class PagePool:
     def add_rows(self, t, unit_tokens=0, clear=False):
         """Register a tensor [batch, ...] with contiguous rows that fork copies, or, with unit_tokens, a
         tensor [batch, heads, units, ...] of which fork copies the first length // unit_tokens units.
-        clear: free sets the rows to zero."""
+        clear: free sets the rows to zero (otherwise they stay)."""
         if t.device != self.device or t.shape[0] != self.page_table.shape[0]:
             raise ValueError("rows are a tensor [batch, ...] on the pool's device")
-        e = t.element_size()
+        e, clear = t.element_size(), L.DASH_ROW_ZERO if clear else L.DASH_ROW_KEPT
         if t.numel() == 0:
             return
         if unit_tokens:
@@ -350,7 +352,7 @@ class PagePool:
         self._pair(self._lib.dash_pages_fork, "dash_pages_fork", src, dst)
 
     def free(self, rows, stream=None):
-        """Empty the rows: pages nobody else holds become free."""
+        """Empty the rows: pages nobody else holds become free; registered caches can fill the rows anew."""
         if _elsewhere(self._index, stream):
             with _within(self.device, stream):
                 return self.free(rows)

@@ -54,6 +54,12 @@ bool rows_ok(const long long st[3])
     return true;
 }
 
+// Whether the tokens and heads of an output [batch, n, h_kv, d] have places of their own.
+bool apart(const dash_params* p, const long long st[3], int n)
+{
+    return (p->batch == 1 || st[0]) && (n == 1 || st[1]) && (p->h_kv == 1 || st[2]);
+}
+
 Shape shape_of(const dash_params* p)
 {
     Shape s = {};
@@ -108,7 +114,8 @@ int check_pages(const dash_pages* pg)
     for (int i = 0; i < pg->num_rows; ++i) {
         const dash_row_array& r = pg->rows[i];
         if (!r.data || r.unit_bytes < 0 || r.heads < 0 || r.max_units < 0 || r.unit_tokens < 0 ||
-            r.unit_bytes > (1ll << 40) || r.row_stride < 0 || r.head_stride < 0)
+            r.unit_bytes > (1ll << 40) || r.row_stride < 0 || r.head_stride < 0 || r.clear < DASH_ROW_KEPT ||
+            r.clear > DASH_ROW_STATE)
             return DASH_EINVAL;
         if (!on(r.data, 4) || (r.unit_bytes | r.row_stride | r.head_stride) % 4) return DASH_EALIGN;
         // a row's runs must not reach into each other or into the next row
@@ -162,6 +169,7 @@ int dash_load_q4(const dash_params* p, const dash_q4_kv* kv, const int* start, i
     if (!on(K, 16) || !on(V, 16) || !rows_ok(p->k_strides) || !rows_ok(p->v_strides)) return DASH_EALIGN;
     if (!on(start, 4) || !on(seqlens, 4)) return DASH_EALIGN;
     if (n == 0) return DASH_OK;
+    if (!apart(p, p->k_strides, n) || !apart(p, p->v_strides, n)) return DASH_EINVAL;
     return status_of(launch_load_q4(shape_of(p), cache_of(kv), start, offset, n, seqlens, K, V, (cudaStream_t)stream));
 }
 

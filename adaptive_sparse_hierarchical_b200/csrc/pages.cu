@@ -472,7 +472,8 @@ __global__ void __launch_bounds__(kMove) free_kernel(PageTab t, const int* rows,
             const long long words = m.max_units * m.unit_bytes / 4;
             for (int h = 0; h < m.heads; ++h)
                 for (long long k = threadIdx.x; k < words; k += kMove)
-                    reinterpret_cast<int*>(m.data + b * m.row_stride + h * m.head_stride)[k] = 0;
+                    reinterpret_cast<uint32_t*>(m.data + b * m.row_stride + h * m.head_stride)[k] =
+                        m.clear == DASH_ROW_STATE && k == words - 2 ? 0xff800000u : 0u;   // -inf
         }
     if (!c.tables) return;
     for (int s = s0 + threadIdx.x; s < s1; s += kMove) {
@@ -494,6 +495,7 @@ MoveRows rows_of(const dash_row_array& p, long long seg)
     m.heads = p.heads;
     m.max_units = p.max_units;
     m.unit_tokens = p.unit_tokens;
+    m.clear = p.clear;
     m.segs = (int)((p.max_units * p.unit_bytes + seg - 1) / seg);
     m.wide = (reinterpret_cast<uintptr_t>(p.data) | (uintptr_t)p.row_stride | (uintptr_t)p.head_stride |
               (uintptr_t)p.unit_bytes) % 16 == 0;

@@ -20,7 +20,7 @@ struct MoveArray {
 struct MoveRows {
     char* data;
     long long row_stride, head_stride, unit_bytes;
-    int heads, max_units, unit_tokens, segs;
+    int heads, max_units, unit_tokens, segs, clear;
     bool wide;
 };
 

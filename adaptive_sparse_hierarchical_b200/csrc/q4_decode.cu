@@ -82,6 +82,15 @@ __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0
 }
 __device__ __forceinline__ uint32_t h2(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
 __device__ __forceinline__ __half2 h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
+// f(512), f(1024), ... below END, as constants
+template <int OFF, int END, typename F>
+__device__ __forceinline__ void each512(const F& f)
+{
+    if constexpr (OFF < END) {
+        f(std::integral_constant<int, OFF>());
+        each512<OFF + 512, END>(f);
+    }
+}
 // (x & MASK) | magic in one instruction (written in C with two constants it becomes two)
 template <uint32_t MASK>
 __device__ __forceinline__ __half2 pick(uint32_t x, uint32_t magic)
@@ -287,11 +296,7 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
                                  "r"(dst + vlane16), "l"(kv.x + lane16), "l"(kv.y + lane16), "r"(meta.nv[k]),
                                  "n"(decltype(off)::value), "n"(St::V + decltype(off)::value));
                 };
-                if constexpr (St::CODES >= 1024) more(std::integral_constant<int, 512>());
-                if constexpr (St::CODES >= 2048) {
-                    more(std::integral_constant<int, 1024>());
-                    more(std::integral_constant<int, 1536>());
-                }
+                each512<512, St::CODES>(more);
             }
             cp_async_commit();
         };

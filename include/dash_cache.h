@@ -88,8 +88,12 @@ typedef struct {                       /* page i: page_bytes at data + i * page_
 
 /* Row i holds `heads` runs of up to max_units units of unit_bytes (a multiple of 4) each, run j at
  * data + i * row_stride + j * head_stride; a row of length L has floor(L / unit_tokens) of them in
- * use (all max_units where unit_tokens is 0).  clear != 0: freeing a row sets its runs to zero (the
- * lengths that further layers keep for themselves). */
+ * use (all max_units where unit_tokens is 0).  clear says what freeing a row leaves in its runs:
+ *   DASH_ROW_KEPT   what was there (summaries: never read beyond a row's length)
+ *   DASH_ROW_ZERO   zeros (the lengths that further layers keep for themselves)
+ *   DASH_ROW_STATE  the state of an empty chunk: each run is one d_h + 2 floats, zeros but for the
+ *                   maximum in the last but one, -inf */
+enum { DASH_ROW_KEPT = 0, DASH_ROW_ZERO = 1, DASH_ROW_STATE = 2 };
 typedef struct {
     void* data;
     long long row_stride, head_stride, unit_bytes;
@@ -124,7 +128,7 @@ int dash_pages_fork(const dash_pages* pg, const int* src, const int* dst, int n,
                     size_t ws_bytes, void* stream);
 
 /* Rows rows[i], i < n (device int32), give up their pages: counts go down, the table rows become
- * -1, the lengths 0 (and the `rows` marked so).  A row listed twice is freed once.  Indices out of
+ * -1, the lengths 0, the `rows` what their `clear` says.  A row listed twice is freed once.  Indices out of
  * range are skipped (and reported). */
 int dash_pages_free(const dash_pages* pg, const int* rows, int n, int* status, void* stream);
 

@@ -83,6 +83,8 @@ def test_bad_calls():
     load = lambda **a: lib.dash_load_q4(*{**dict(p=p, kv=kv, st=256, o=0, n=3, sl=256, k=256, v=256, s=None), **a}.values())   # noqa: E731
     for name in ("k", "v", "sl"):
         assert load(**{name: None}) == L.DASH_EINVAL
+    assert load(p=_p(k_strides=(1024 * 256, 0, 128))) == L.DASH_EINVAL        # every token in one place
+    assert load(p=_p(v_strides=(0, 256, 128))) == L.DASH_EINVAL
     assert load(n=-1) == L.DASH_EINVAL and load(v=260) == L.DASH_EALIGN and load(n=0) == L.DASH_OK
     dec = lambda **a: lib.dash_decode_q4(*{**dict(p=p, kv=kv, q=256, kb=256, sl=256, o=256, r=None, w=256, n=ws, s=None),   # noqa: E731
                                            **a}.values())
@@ -119,7 +121,7 @@ A, W = L.dash_page_array, L.dash_row_array
     (_pg(rows=[W(None, 64, 16, 16, 2, 1, 0, 0)]), L.DASH_EINVAL), (_pg(rows=[W(256, 62, 16, 16, 2, 1, 0, 0)]), L.DASH_EALIGN),
     (_pg(rows=[W(256, 64, 16, 16, 2, 2, 0, 0)]), L.DASH_EINVAL),    # runs overlap
     (_pg(rows=[W(256, 32, 32, 16, 2, 2, 32, 0)]), L.DASH_EINVAL),   # rows overlap
-    (_pg(rows=[W(256, 64, 16, 16, -1, 1, 0, 0)]), L.DASH_EINVAL),
+    (_pg(rows=[W(256, 64, 16, 16, -1, 1, 0, 0)]), L.DASH_EINVAL), (_pg(rows=[W(256, 64, 16, 16, 2, 1, 0, 3)]), L.DASH_EINVAL),
 ])
 def test_bad_pages(pg, code):
     lib, ws = D.load(), 1 << 40
@@ -137,6 +139,9 @@ def test_bad_page_calls():
     assert lib.dash_pages_copy(pg, None, 256, 2, 256, 256, ws, None) == L.DASH_EINVAL
     assert lib.dash_pages_copy(pg, 256, 256, -1, 256, 256, ws, None) == L.DASH_EINVAL
     assert lib.dash_pages_fork(pg, 256, 256, 5, 256, 256, ws, None) == L.DASH_EINVAL      # more than there are rows
+    many = _pg(batch=2000)
+    ws2 = lib.dash_pages_workspace_size(many)
+    assert lib.dash_pages_fork(many, 256, 256, 1025, 256, 256, ws2, None) == L.DASH_EUNSUPPORTED
     assert lib.dash_pages_free(pg, None, 1, 256, None) == L.DASH_EINVAL
     assert lib.dash_pages_free(pg, 258, 1, 256, None) == L.DASH_EALIGN
     assert lib.dash_pages_copy(pg, 256, 256, 1, 256, 256, ws - 1, None) == L.DASH_EWORKSPACE

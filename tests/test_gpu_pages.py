@@ -261,7 +261,7 @@ def test_many_arrays():
 def _serve(kind, layers, graph):
     """Prefill, fork, decode, free, compact, decode: rows over shared pages give what a private cache gives."""
     b, cap, hq, hkv, d, B = 6, 512, 8, 2, 128, 64
-    slots, pages = cap // PAGE, 30
+    slots, pages = cap // PAGE, 40
     table = torch.full((b, slots), -1, dtype=torch.int32, device="cuda")
     g = torch.Generator(device="cuda").manual_seed(5)
     rnd = lambda *s: torch.randn(*s, device="cuda", generator=g).bfloat16()   # noqa: E731
@@ -316,12 +316,13 @@ def _serve(kind, layers, graph):
             continue
         t.state[[0, 3]] = 0
         t.state[[0, 3], :, d] = -torch.inf
-    if kind != "q4":
-        for s in shared:
-            s.state[[0, 3]] = 0
-            s.state[[0, 3], :, d] = -torch.inf
-    live = [1, 2, 4, 5]
-    assert steps(40)
+    for s in shared:   # the freed rows are empty in every layer
+        assert not s.seqlens[[0, 3]].any() and (s.state[[0, 3], :, d] == -torch.inf).all() and not s.state[[0, 3], :, :d].any()
+    live = [0, 1, 2, 3, 4, 5]
+    assert steps(70)   # the emptied rows start over, past a chunk's end
+    for s, t in zip(shared, alone):
+        for i, n in enumerate(s.seqlens.tolist()):
+            assert torch.equal(s.kbar[i, :, : n // B], t.kbar[i, :, : n // B]) and torch.equal(s.state[i], t.state[i])
     pool.check()
 
 
@@ -350,3 +351,75 @@ def test_captured_run():
         assert m.fork(s, [2, 3, 5]) is None and m.reserve([30] * 6) is None
         _same(pool, m, a, wide)
     pool.check()
+
+
+def test_fork_in_a_large_batch():
+    """More rows than a plan's shared memory marks, all 1024 entries of a call, and the marks' checks there."""
+    m = Model(5000, 2, 3000)
+    m.reserve([100 if b < 40 else 0 for b in range(5000)])
+    m.lens[:40] = 100
+    pool, a, wide, *_ = _pool(m)
+    src, dst = [i % 40 for i in range(1024)], list(range(4999, 4999 - 1024, -1))
+    pool.fork(src, dst)
+    m.fork(src, dst)
+    _same(pool, m, a, wide)
+    pool.check()
+    pool.fork([0, 1, 2], [50, 60, 50])
+    _same(pool, m, a, wide)
+    with pytest.raises(D.DashError, match="twice"):
+        pool.check()
+
+
+def test_rows_of_odd_units():
+    """Row arrays whose runs are copied word by word, several heads, ragged lengths."""
+    m = Model(4, 3, 12)
+    m.reserve([100, 30, 0, 0])
+    m.lens[:] = [100, 30, 0, 0]
+    pool, a, wide, *_ = _pool(m)
+    t = torch.randint(0, 1000, (4, 3, 6, 3), dtype=torch.int32, device="cuda")
+    pool.add_rows(t, unit_tokens=32)
+    want = t.clone()
+    pool.fork([0, 1], [3, 2])
+    m.fork([0, 1], [3, 2])
+    want[3, :, :3] = want[0, :, :3]
+    assert torch.equal(t, want)
+    _same(pool, m, a, wide)
+
+
+def test_refused_registrations():
+    m = Model(3, 2, 6)
+    pool, *_ = _pool(m)
+    for bad in (torch.zeros(5, 4, device="cuda"), torch.zeros(6, 4), torch.zeros(6, 3, device="cuda"),
+                torch.zeros(6, 4, 4, device="cuda").transpose(1, 2), torch.zeros(1, 4, device="cuda").expand(6, 4)):
+        with pytest.raises(ValueError):
+            pool.add_pages(bad)
+    for bad in (torch.zeros(2, 4, device="cuda"), torch.zeros(3, 4, 4, device="cuda").transpose(1, 2),
+                torch.zeros(1, 4, device="cuda").expand(3, 4), torch.zeros(3, 3, dtype=torch.int16, device="cuda")):
+        with pytest.raises(ValueError):
+            pool.add_rows(bad)
+    with pytest.raises(TypeError):
+        pool.free(torch.tensor([1], device="cuda"))
+    with pytest.raises(ValueError):
+        pool.fork([0, 1], [2])
+    pool.free([0])
+    pool.check()
+
+
+def test_lists_on_another_stream():
+    """Calls on a stream of their own take their lists there too."""
+    m = Model(4, 3, 12)
+    m.reserve([100, 64, 0, 0])
+    m.lens[:] = [100, 64, 0, 0]
+    pool, a, wide, *_ = _pool(m)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    pool.fork([0, 1], [2, 3], stream=stream)
+    pool.reserve(50, stream=stream)
+    pool.free([0], stream=stream.cuda_stream)
+    pool.compact(stream=stream)
+    torch.cuda.current_stream().wait_stream(stream)
+    m.fork([0, 1], [2, 3])
+    m.reserve([50] * 4)
+    m.free([0])
+    m.compact()
+    _same(pool, m, a, wide)

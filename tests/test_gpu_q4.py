@@ -254,6 +254,10 @@ CASES = [
     (16, 1, 64, 64, 64, [700, 64, 3]),
     (16, 16, 64, 16, 16, [100, 257]),
     (64, 8, 128, 32, 32, [40, 0, 1111]),
+    (16, 1, 128, 16, 64, [333, 16]),
+    (4, 1, 128, 16, 32, [17, 200, 0, 15]),
+    (16, 1, 64, 16, 16, [100, 1]),
+    (16, 4, 64, 128, 128, [128, 129, 1500]),
 ]
 
 
@@ -410,3 +414,135 @@ def test_matches_bf16_cache_routes():
     # 4 bits with groups of 32: about a tenth of the values' size per key and value, averaged down
     far = sum((a - c).norm() for a, c in outs) / sum(c.norm() for _, c in outs)
     assert far < 0.25, far
+
+
+def test_decode_more_pairs_than_blocks():
+    """More (sequence, KV head) pairs than the GPU has room for blocks, some of them empty."""
+    rng = np.random.default_rng(20)
+    b, hq, hkv, d, B, page = 130, 16, 4, 64, 32, 64
+    lens = [int(n) for n in rng.integers(0, 140, b)]
+    lens[5], lens[6] = 0, 1
+    st = _state(rng, b, 192, hq, hkv, d, chunk=B, page=page, gamma=0.0)
+    K, V = _fill_ref(rng, b, lens, hkv, d)
+    st.fill(K.cuda(), V.cuda(), lens)
+    q = _bf16(rng, b, hq, d)
+    ref, err = _decode_ref(st, q.double().numpy(), K.double().numpy(), V.double().numpy(), lens, hq, hkv, d, B, None, 0, 0)
+    _check_out(st.decode(q.cuda()), ref, err)
+    st.seqlens.zero_()
+    assert not st.decode(q.cuda()).any()      # nothing cached at all
+
+
+@pytest.mark.parametrize("size", [1e-37, 1e-3, 1e3, 1e30])
+def test_query_sizes(size):
+    """Queries of any size: with keys to match, the softmax is the same."""
+    rng = np.random.default_rng(21)
+    hq, hkv, d, B, page, n = 8, 1, 128, 64, 64, 300
+    st = _state(rng, 1, 320, hq, hkv, d, chunk=B, page=page, gamma=0.0)
+    K, V = _bf16(rng, 1, n, hkv, d), _bf16(rng, 1, n, hkv, d)
+    st.fill(K.cuda(), V.cuda(), [n])
+    q = _bf16(rng, 1, hq, d, scale=size)
+    q[0, 1], q[0, 2, 5:] = 0, 0           # a head without a query: the mean of the values; one of few elements
+    q[0, 3, 7] = size * 1e-6              # elements of very different size
+    if size > 1e29:
+        q[0, 0] = 0
+        q[0, 0, 0] = 3e38                 # logits beyond fp32
+    ref, err = _decode_ref(st, q.double().numpy(), K.double().numpy(), V.double().numpy(), [n], hq, hkv, d, B, None, 0, 0)
+    o = st.decode(q.cuda())
+    _check_out(o[:, 1:2], ref[:, 1:2], err[:, 1:2])
+    if size < 1e29:
+        _check_out(o, ref, err)
+
+
+def test_nonfinite_queries_stay_in_their_heads():
+    rng = np.random.default_rng(22)
+    hq, hkv, d, B, page, n = 16, 1, 64, 32, 32, 100
+    st = _state(rng, 2, 128, hq, hkv, d, chunk=B, page=page, gamma=0.0)
+    K, V = _bf16(rng, 2, n, hkv, d), _bf16(rng, 2, n, hkv, d)
+    st.fill(K.cuda(), V.cuda(), [n, n])
+    q = _bf16(rng, 2, hq, d).cuda()
+    clean = st.decode(q).clone()
+    q[0, 3, 10], q[1, 9, 0] = NAN, float("inf")
+    o = st.decode(q)
+    assert torch.isnan(o[0, 3]).all() and torch.isnan(o[1, 9]).all()
+    keep = torch.ones(2, hq, dtype=torch.bool)
+    keep[0, 3] = keep[1, 9] = False
+    assert torch.equal(o[keep], clean[keep])
+
+
+def test_far_pages():
+    """A pool whose pages lie more than 2^31 bytes apart, and page strides larger than a page."""
+    rng = np.random.default_rng(23)
+    hq, hkv, d, B, page, n = 4, 2, 128, 64, 64, 200
+    st = _state(rng, 1, 256, hq, hkv, d, chunk=B, page=page, gamma=0.0, slack=0)
+    near = _state(np.random.default_rng(23), 1, 256, hq, hkv, d, chunk=B, page=page, gamma=0.0, slack=0)
+    size = hkv * page * d // 2
+    stride = (1 << 30) + 4096
+    far = torch.zeros(3 * stride + size, dtype=torch.uint8, device="cuda")
+    st.k_codes = torch.as_strided(far, (4, hkv, page, d // 2), (stride, page * d // 2, d // 2, 1))
+    st.kv = D.q4_kv(st.k_codes, st.k_scales, st.v_codes, st.v_scales, st.page_table, page_size=page)
+    st.qbar = near.qbar
+    K, V = _bf16(rng, 1, n, hkv, d).cuda(), _bf16(rng, 1, n, hkv, d).cuda()
+    q = _bf16(rng, 1, hq, d).cuda()
+    outs = []
+    for s in (st, near):
+        s.fill(K, V, [n])
+        outs.append((s.decode(q).clone(), *s.load(0, n)))
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
+    pool = D.PagePool.of([near])
+    far_pool = D.PagePool.of([st])
+    for s, p in ((near, pool), (st, far_pool)):
+        p.refs.zero_()
+        p.copy([s.page_table[0, 0].item()], [s.page_table[0, 1].item()])
+    assert torch.equal(st.load(0, n)[0], near.load(0, n)[0])
+
+
+def test_refusals():
+    rng = np.random.default_rng(24)
+    st = _state(rng, 2, 128, 4, 2, 64, chunk=32, page=32)
+    k = _bf16(rng, 2, 3, 2, 64).cuda()
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")   # noqa: E731
+    for bad in (lambda: st.append(k.float(), k), lambda: st.append(k.cpu(), k), lambda: st.append(k, k, ints(1, 2).long()),
+                lambda: st.append(k, None), lambda: st.decode(k), lambda: st.decode(st.O.float()), lambda: st.load(ints(0, 0).cpu(), 3),
+                lambda: st.append(k[0, 0], k[0, 0])):
+        with pytest.raises((TypeError, ValueError)):
+            bad()
+    for bad in (lambda: st.append(k, k[:, :2]), lambda: st.append(k[:1], k[:1]), lambda: st.append(k, k, ints(1)),
+                lambda: st.append(k.transpose(2, 3), k.transpose(2, 3)), lambda: st.append(k, k, ints(1, 0, 2, 0)[::2]),
+                lambda: st.load(ints(0), 3), lambda: st.load(0, 3, k[:, :2], k), lambda: st.decode(torch.zeros_like(st.O).transpose(0, 1))):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(D.DashError):
+        st.load(0, 3, k[:, :1].expand(-1, 3, -1, -1), k)      # all tokens in one place
+    with pytest.raises(D.DashError):
+        st.append(torch.zeros(2, 3, 2, 68, dtype=torch.bfloat16, device="cuda")[..., :64], k)   # rows 136 bytes apart
+    big = D.Q4DecodeState(2, 64, 2, 1, 64, chunk=32, alpha=3.0, gamma=1.0, page_size=32)
+    with pytest.raises(D.DashError):
+        big.decode(big.O.clone())
+
+
+def test_dense_needs_no_room_for_routing():
+    """Chunk logits of 16 heads x 4096 chunks do not fit the routing's shared memory; dense decoding has none."""
+    rng = np.random.default_rng(25)
+    hq, hkv, d, B, page, n = 16, 1, 64, 32, 64, 500
+    kw = dict(chunk=B, page=page)
+    st = _state(rng, 1, 131072, hq, hkv, d, gamma=0.0, **kw)
+    K, V = _bf16(rng, 1, n, hkv, d), _bf16(rng, 1, n, hkv, d)
+    st.fill(K.cuda(), V.cuda(), [n])
+    q = _bf16(rng, 1, hq, d)
+    ref, err = _decode_ref(st, q.double().numpy(), K.double().numpy(), V.double().numpy(), [n], hq, hkv, d, B, None, 0, 0)
+    _check_out(st.decode(q.cuda()), ref, err)
+    st = _state(rng, 1, 131072, hq, hkv, d, gamma=1.0, **kw)
+    with pytest.raises(D.DashError):
+        st.decode(q.cuda())
+
+
+def test_load_and_append_nothing():
+    st = _state(np.random.default_rng(26), 2, 64, 2, 1, 64, chunk=32, page=32)
+    K, V = st.load(0, 0)
+    assert K.shape == V.shape == (2, 0, 1, 64)
+    k = torch.ones(2, 8, 1, 64, dtype=torch.bfloat16, device="cuda")
+    st.append(k, k, torch.zeros(2, dtype=torch.int32, device="cuda"))
+    st.fill(k, k, [0, 0])
+    assert not st.seqlens.any() and not st.k_scales.any() and (st.state[..., 64] == -torch.inf).all()
+    assert not st.load(0, 64)[0].any()
