@@ -13,6 +13,9 @@ cudaError_t launch_load_q4(const Shape& s, const Q4& c, const int* start, int of
                            void* K, void* V, cudaStream_t st);
 cudaError_t launch_attend_q4(const Shape& s, const Q4& c, const void* q, const int* seqlens, const Routes& rt, bool dense,
                              float* part, int* span, void* O, cudaStream_t st);
+bool route_q4_supported(const Shape& s);
+cudaError_t launch_route_q4(const Shape& s, const void* q, const float* kbar, const int* seqlens, const Routes& rt,
+                            float* X, int* status, cudaStream_t st);
 int q4_max_pairs();
 size_t q4_part_floats(const Shape& s);
 
@@ -93,7 +96,7 @@ Q4Layout q4_layout(const dash_params* p)
     L.idx = L.counts + up(bh * 4);
     L.bias = L.idx + up(bh * T * 4);
     L.x = L.bias + up(bh * T * 4);
-    L.err = L.x + (p->gamma > 0.f ? up(bh * s.g * T * 4) : 0);
+    L.err = L.x + up(bh * s.g * T * 4);
     L.total = L.err + kAlign;
     return L;
 }
@@ -199,8 +202,11 @@ int dash_decode_q4(const dash_params* p, const dash_q4_kv* kv, const void* q, co
     rt.words = (s.T + 31) / 32;
     if (!on(rt.counts, 4) || !on(rt.idx, 4) || !on(rt.bias, 4) || !on(rt.bitmask, 4)) return DASH_EALIGN;
     if (routed) {
-        rc = status_of(launch_route_decode(s, p->dtype, q, kbar_cache, s.T, seqlens, rt, (float*)(ws + L.x),
-                                           (int*)(ws + L.err), (cudaStream_t)stream));
+        float* X = (float*)(ws + L.x);
+        int* err = (int*)(ws + L.err);
+        rc = status_of(route_q4_supported(s)
+                           ? launch_route_q4(s, q, kbar_cache, seqlens, rt, X, err, (cudaStream_t)stream)
+                           : launch_route_decode(s, p->dtype, q, kbar_cache, s.T, seqlens, rt, X, err, (cudaStream_t)stream));
         if (rc != DASH_OK) return rc;
     }
     return status_of(launch_attend_q4(s, cache_of(kv), q, seqlens, rt, dense, (float*)(ws + L.part), (int*)(ws + L.span), O,

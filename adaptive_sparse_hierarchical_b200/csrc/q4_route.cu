@@ -1,0 +1,344 @@
+// q4_route.cu -- Stage 1 of decoding for the 4-bit cache's decode: chunk logits over the whole GPU, then
+// thresholds and route lists with the heads of a group spread over a cluster.
+//
+// The quantities are those of stage1_decode.cu (Eq. 6 and Proposition 4.1):
+//   x_c^(h) = (alpha-1) gamma <q^(h), kbar_c>/sqrt(d),  what = [x - tau]_+^{1/(alpha-1)},  w = mean over heads,
+//   R = {w > 0},  bias_c = (log w_c - mean_R log w)/sigma
+// and the logits are the same numbers (the same MMAs on the exact three-plane split of kbar).  There one
+// cluster does all of it for a (sequence, KV head), which leaves most SMs idle while the summaries are read
+// and has every head's threshold solved on a list that crosses blocks.  Here
+//   1. a warp takes 16 chunks of a pair, reads their summaries once (all loads in flight together) and
+//      writes the group's logits: HBM-bound, 4 d bytes per chunk;
+//   2. in a cluster of 4 blocks per pair each block owns a quarter of the heads and keeps their whole rows in
+//      registers: a Newton step is one pass over registers and one block barrier.  The heads' weights take the
+//      logits' place (in L2: reading them from the other blocks' shared memory took twice as long), and block
+//      k adds them up for the k-th quarter of the chunks.
+#include <cooperative_groups.h>
+
+#include "entmax.cuh"
+#include "q4.cuh"
+#include "stage2_mma.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace dash {
+namespace {
+
+constexpr int kLogitWarps = 8, kTiles = 2;   // 8-chunk tiles per warp
+constexpr int kCl = 4, kThr = 512, kWarps = kThr / 32, kMaxVals = 32;
+
+// (hi, mid, lo) bf16 pairs with hi + mid + lo == (x0, x1) exactly, by truncation.
+__device__ __forceinline__ void split3(float2 x, uint32_t& hi, uint32_t& mid, uint32_t& lo)
+{
+    const float h0 = __uint_as_float(__float_as_uint(x.x) & 0xffff0000u), h1 = __uint_as_float(__float_as_uint(x.y) & 0xffff0000u);
+    const float r0 = x.x - h0, r1 = x.y - h1;
+    const float m0 = __uint_as_float(__float_as_uint(r0) & 0xffff0000u), m1 = __uint_as_float(__float_as_uint(r1) & 0xffff0000u);
+    hi = __byte_perm(__float_as_uint(h0), __float_as_uint(h1), 0x7632);
+    mid = __byte_perm(__float_as_uint(m0), __float_as_uint(m1), 0x7632);
+    lo = __byte_perm(__float_as_uint(r0 - m0), __float_as_uint(r1 - m1), 0x7632);
+}
+
+__device__ __forceinline__ int chunks_of(const Shape& s, const int* seqlens, int b)
+{
+    return max(0, min((seqlens[b] - 1) / s.B, s.T));
+}
+
+// X [pair][head][T]: the logits of the complete chunks before each query's own.
+template <int D>
+__global__ void __launch_bounds__(32 * kLogitWarps) route_logits_kernel(Shape s, const __nv_bfloat16* __restrict__ q,
+                                                                        const float* __restrict__ kbar,
+                                                                        const int* __restrict__ seqlens, float* X)
+{
+    pdl_wait();   // the append of this step
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3, G = s.g;
+    const unsigned per = (s.T + 8 * kTiles - 1) / (8 * kTiles);
+    const unsigned unit = blockIdx.x * kLogitWarps + warp;   // at most 2048 pairs x 57600 chunks / 16
+    if (unit >= (unsigned)(s.batch * s.hkv) * per) return;
+    const int br = unit / per, c0 = (unit % per) * 8 * kTiles, b = br / s.hkv, r = br % s.hkv;
+    const int nv = chunks_of(s, seqlens, b);
+    if (c0 >= nv) return;
+    const float* kb = kbar + ((long long)br * s.T + c0 + g8) * D + 2 * t4;
+    float2 u[kTiles][D / 16][2];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const bool on = c0 + t * 8 + g8 < nv;
+            const float* p = kb + t * 8 * D + kk * 16;
+            u[t][kk][0] = on ? __ldg(reinterpret_cast<const float2*>(p)) : make_float2(0.f, 0.f);
+            u[t][kk][1] = on ? __ldg(reinterpret_cast<const float2*>(p + 8)) : make_float2(0.f, 0.f);
+        }
+    uint32_t qf[D / 16][4];
+    const __nv_bfloat16* qb = q + ((long long)b * s.hq + r * G) * D;
+    load_q_frags<D>(qf, [&](int h) -> const __nv_bfloat16* { return h < G ? qb + (long long)h * D : nullptr; });
+    const float xs = (s.alpha - 1.f) * s.gamma * rsqrtf((float)D);
+    float* out = X + (long long)br * G * s.T;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t h0, m0, l0, h1, m1, l1;
+            split3(u[t][kk][0], h0, m0, l0);
+            split3(u[t][kk][1], h1, m1, l1);
+            mma_bf16(acc, qf[kk], l0, l1);
+            mma_bf16(acc, qf[kk], m0, m1);
+            mma_bf16(acc, qf[kk], h0, h1);
+        }
+        const int c = c0 + t * 8 + 2 * t4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int h = g8 + (e >> 1) * 8;
+            if (h < G && c + (e & 1) < nv) out[(long long)h * s.T + c + (e & 1)] = acc[e] * xs;
+        }
+    }
+}
+
+struct Cross {     // what a block tells the others of its cluster about its quarter of the chunks
+    float slog;    // sum of log w over the routed ones
+    int cnt;
+};
+
+// heads_per_block heads share the block's 16 warps; a head takes as few of its warps (a power of two) as
+// keep 8 entries or less per thread: the fewer, the less there is to add up in a step, and a head in a
+// single warp needs no barrier at all.
+__host__ __device__ inline int heads_per_block(int g) { return (g + kCl - 1) / kCl; }
+__host__ __device__ inline int warps_per_head(int g, int T)
+{
+    const int most = kWarps / heads_per_block(g);   // g is a power of two: so is this
+    int w = 1;
+    while (w < most && T > 8 * 32 * w) w *= 2;
+    return w;
+}
+inline int vals_per_thread(const Shape& s)
+{
+    const int lanes = 32 * warps_per_head(s.g, s.T);
+    return (s.T + lanes - 1) / lanes;
+}
+
+// Chunks per block in the last phase: whole 32-chunk words.
+__host__ __device__ inline int quarter(int nv) { return ((nv + kCl - 1) / kCl + 31) / 32 * 32; }
+
+// u^p for u >= 0, kept out of line: alpha other than 1.5 and 2 is rare, and code that is only passed over
+// has to be fetched too (these kernels run once per call, from a cold instruction cache).
+__device__ __noinline__ float power(float u, float p) { return u > 0.f ? exp2f(p * __log2f(u)) : 0.f; }
+
+// f = sum u^p, fd = sum u^(p-1) over the entries u = v - t > 0 of this thread.
+template <int V>
+__device__ __forceinline__ void sums(const float* v, float t, float p, int mode, float& f, float& fd)
+{
+    if (mode == 2) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const float u = fmaxf(v[k] - t, 0.f);
+            fd += u;
+            f = fmaf(u, u, f);
+        }
+    } else if (mode == 1) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const float u = fmaxf(v[k] - t, 0.f);
+            f += u;
+            fd += u > 0.f ? 1.f : 0.f;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const float u = fmaxf(v[k] - t, 0.f);
+            if (u > 0.f) { f += power(u, p); fd += power(u, p - 1.f); }
+        }
+    }
+}
+
+// One Newton step of the threshold solve (ent_step of entmax.cuh without its closed forms, on the fast
+// divide and square root: a step corrects what the one before was off by).  f, fd: sums of u^p and u^(p-1).
+__device__ __forceinline__ bool newton(float f, float fd, float& t, float& lo, float& hi, float alpha, int mode)
+{
+    if (f >= 1.f) lo = t;
+    else hi = t;
+    float tn = 0.5f * (lo + hi);
+    if (fd > 0.f && f > 0.f) {
+        float g;
+        if (mode == 2) asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(g) : "f"(f));
+        else g = mode == 1 ? f : exp2f((alpha - 1.f) * __log2f(f));
+        tn = t + __fdividef((g - 1.f) * f, g * fd);
+    }
+    if (fabsf(tn - t) <= 2e-7f * fmaxf(1.f, fabsf(t)) || fabsf(f - 1.f) <= 1e-6f) {
+        t = tn;
+        return true;
+    }
+    t = tn > lo && tn < hi ? tn : 0.5f * (lo + hi);
+    return false;
+}
+
+template <int V>
+__global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThr, 1)
+    route_solve_kernel(Shape s, float* X, const int* __restrict__ seqlens, Routes rt, int* status)
+{
+    extern __shared__ float keep[];   // the weights of this block's quarter of the chunks
+    __shared__ float red[kWarps], lsum[kWarps];
+    __shared__ float2 part[2][kWarps];
+    __shared__ int csum[kWarps];
+    __shared__ Cross cx;
+    cg::cluster_group cl = cg::this_cluster();
+    pdl_wait();
+    pdl_launch_dependents();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
+    const int rank = (int)cl.block_rank(), br = blockIdx.x / kCl, b = br / s.hkv, G = s.g;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int nv = chunks_of(s, seqlens, b);
+    const int hb = heads_per_block(G), wph = warps_per_head(G, s.T);
+    const int hl = warp / wph, h = rank * hb + hl, sub = (warp & (wph - 1)) * 32 + lane, step = wph * 32;
+    const bool mine = hl < hb && h < G, active = mine && nv > 0;
+    const float p = 1.f / (s.alpha - 1.f);
+    const int mode = ent_mode(s.alpha);
+
+    // ---- this thread's logits of head h; the head's maximum --------------------------------------
+    float v[V], mx = -INFINITY;
+    float* row = X + ((long long)br * G + h) * s.T;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        v[k] = active && sub + k * step < nv ? row[sub + k * step] : -INFINITY;
+        mx = fmaxf(mx, v[k]);
+    }
+    mx = warp_max(mx);
+    if (wph > 1) {
+        if (lane == 0) red[warp] = mx;
+        __syncthreads();
+        for (int k = 0; k < wph; ++k) mx = fmaxf(mx, red[(hl * wph + k) & (kWarps - 1)]);
+    }
+
+    // ---- threshold: Newton steps from max - 1, at most one barrier each ---------------------------
+    float lo = mx - 1.f, t = lo, hi = active ? mx - exp2f(-(s.alpha - 1.f) * __log2f((float)nv)) : 0.f;
+    bool done = !active;
+    for (int it = 0; it < kMaxIter; ++it) {
+        float f = 0.f, fd = 0.f;
+        if (!done) {
+            sums<V>(v, t, p, mode, f, fd);
+            f = warp_sum(f);
+            fd = warp_sum(fd);
+        }
+        if (wph > 1) {
+            if (lane == 0 && !done) part[it & 1][warp] = make_float2(f, fd);
+            if (__syncthreads_and(done)) break;   // a buffer is written again two steps, and a barrier, later
+            f = fd = 0.f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                if (k >= wph) break;
+                const float2 o = part[it & 1][(hl * wph + k) & (kWarps - 1)];
+                f += o.x;
+                fd += o.y;
+            }
+        } else if (done) {
+            break;
+        }
+        if (!done) done = newton(f, fd, t, lo, hi, s.alpha, mode);
+    }
+    if (mine)
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            if (sub + k * step < nv) {
+                const float u = fmaxf(v[k] - t, 0.f);
+                __stcg(row + sub + k * step, mode == 2 ? u * u : mode == 1 ? u : power(u, p));   // over the logit
+            }
+    cl.sync();
+
+    // ---- group weights of this block's quarter of the chunks, in whole 32-chunk words --------------
+    const int per = quarter(nv), c_lo = min(nv, rank * per), c_hi = min(nv, c_lo + per);
+    const int each = ((c_hi - c_lo + kWarps - 1) / kWarps + 31) / 32 * 32;   // a warp's part, in words too
+    const int w_lo = min(c_hi, c_lo + warp * each), w_hi = min(c_hi, w_lo + each);
+    const float inv_g = 1.f / G;
+    const float* wrow = X + (long long)br * G * s.T;
+    auto weight = [&](int c) {   // the heads in order; the reads are on their way before the first is added
+        float a[16], sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) a[k] = k < G ? __ldcg(wrow + (long long)k * s.T + c) : 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) sum += a[k];
+        return sum * inv_g;
+    };
+    float sl = 0.f;
+    int cn = 0;
+#pragma unroll 1
+    for (int c = w_lo + lane; c < w_hi; c += 32) {
+        const float w = weight(c);
+        keep[c - c_lo] = w;
+        if (w > 0.f) { sl += __logf(w); ++cn; }
+    }
+    sl = warp_sum(sl);
+    cn = warp_isum(cn);
+    if (lane == 0) { lsum[warp] = sl; csum[warp] = cn; }
+    __syncthreads();
+    if (tid == 0) {
+        float a = 0.f;
+        int n = 0;
+        for (int k = 0; k < kWarps; ++k) { a += lsum[k]; n += csum[k]; }
+        cx.slog = a;
+        cx.cnt = n;
+    }
+    cl.sync();
+    float tot_log = 0.f;
+    int tot = 0, at = 0;
+    for (int k = 0; k < kCl; ++k) {
+        const Cross* o = cl.map_shared_rank(&cx, k);
+        tot_log += o->slog;
+        if (k < rank) at += o->cnt;
+        tot += o->cnt;
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // done with the others' memory
+    for (int k = 0; k < warp; ++k) at += csum[k];
+    const float mu = tot > 0 ? tot_log / tot : 0.f;
+
+    // ---- ascending lists ---------------------------------------------------------------------------
+    int* idx = rt.idx + (long long)br * rt.cap;
+    float* bias = rt.bias + (long long)br * rt.cap;
+    uint32_t* mrow = rt.bitmask ? rt.bitmask + (long long)br * rt.words : nullptr;
+#pragma unroll 1
+    for (int c0 = w_lo; c0 < w_hi; c0 += 32) {
+        const int c = c0 + lane;
+        const float w = c < w_hi ? keep[c - c_lo] : 0.f;
+        const bool on = w > 0.f;
+        const uint32_t m = __ballot_sync(0xffffffffu, on);
+        if (on) {
+            const int j = at + __popc(m & ((1u << lane) - 1u));
+            idx[j] = c;
+            bias[j] = (__logf(w) - mu) * s.inv_sigma;
+        }
+        if (mrow && lane == 0) mrow[c0 >> 5] = m;
+        at += __popc(m);
+    }
+    if (rank == 0) {
+        if (tid == 0) rt.counts[br] = tot;
+        if (mrow)
+            for (int wd = ((nv + 31) >> 5) + tid; wd < rt.words; wd += kThr) mrow[wd] = 0u;
+    }
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // no block leaves while its memory is read
+}
+
+template <int V>
+cudaError_t solve_t(const Shape& s, float* X, const int* seqlens, const Routes& rt, int* status, cudaStream_t st)
+{
+    return launch_after(route_solve_kernel<V>, dim3(kCl * s.batch * s.hkv), dim3(kThr), quarter(s.T) * 4, st, s, X,
+                        seqlens, rt, status);
+}
+
+}  // namespace
+
+// A thread holds at most 32 entries, a block the weights of a quarter of the chunks (static shared memory aside).
+bool route_q4_supported(const Shape& s) { return s.T > 0 && vals_per_thread(s) <= kMaxVals && quarter(s.T) * 4 <= 46 * 1024; }
+
+cudaError_t launch_route_q4(const Shape& s, const void* q, const float* kbar, const int* seqlens, const Routes& rt,
+                            float* X, int* status, cudaStream_t st)
+{
+    const long long units = (long long)s.batch * s.hkv * ((s.T + 8 * kTiles - 1) / (8 * kTiles));
+    const dim3 grid((unsigned)((units + kLogitWarps - 1) / kLogitWarps));
+    const cudaError_t e = launch_after(s.d == 128 ? route_logits_kernel<128> : route_logits_kernel<64>, grid,
+                                       dim3(32 * kLogitWarps), 0, st, s, (const __nv_bfloat16*)q, kbar, seqlens, X);
+    if (e != cudaSuccess) return e;
+    const int v = vals_per_thread(s);
+    return v <= 4 ? solve_t<4>(s, X, seqlens, rt, status, st)
+                  : v <= 16 ? solve_t<16>(s, X, seqlens, rt, status, st) : solve_t<kMaxVals>(s, X, seqlens, rt, status, st);
+}
+
+}  // namespace dash

@@ -7,9 +7,12 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import adaptive_sparse_hierarchical_b200 as D
+from adaptive_sparse_hierarchical_b200 import inputs
 
 import q4_ref as R
+from parity import bias_tolerance, check_routes
 
 pytestmark = pytest.mark.gpu
 
@@ -546,3 +549,44 @@ def test_load_and_append_nothing():
     st.fill(k, k, [0, 0])
     assert not st.seqlens.any() and not st.k_scales.any() and (st.state[..., 64] == -torch.inf).all()
     assert not st.load(0, 64)[0].any()
+
+
+@pytest.mark.parametrize("g,hkv,d,B,cap,lens,alpha,gamma,inv_sigma", [
+    (8, 2, 128, 64, 2048, [2000, 65, 64], 1.5, 6.0, 1.0),          # a warp per head, few entries
+    (4, 2, 128, 32, 8192, [8000, 1], 2.0, 4.0, 0.5),
+    (2, 1, 64, 16, 4096, [4095, 17, 4081], 1.25, 3.0, 1.0),
+    (1, 2, 64, 16, 16384, [16000, 9000], 1.5, 8.0, 0.0),           # 4 warps per head
+    (16, 1, 128, 16, 32768, [32768, 20000], 1.5, 5.0, 1.0),
+    (16, 1, 64, 16, 57600, [57000, 40], 2.0, 5.0, 1.0),            # 32 entries per thread
+    (8, 1, 64, 16, 40000, [39990], 1.8, 2.0, 1.0),
+    (1, 1, 64, 16, 320000, [310000], 1.5, 8.0, 1.0),               # more than the cluster's registers hold
+])
+def test_routes_against_the_oracle(g, hkv, d, B, cap, lens, alpha, gamma, inv_sigma):
+    """Routed sets by the margin rule, biases within what the logits' error does to log w, bitmask, for every way the
+    routing splits its work."""
+    b, T = len(lens), cap // B
+    x = inputs.planted(77, b, cap, g * hkv, hkv, d, B, dtype="bf16", chunk_frac=0.05)
+    st = D.Q4DecodeState(b, cap, g * hkv, hkv, d, chunk=B, alpha=alpha, gamma=gamma, inv_sigma=inv_sigma, page_size=B * 4,
+                         qbar=torch.from_numpy(x["qbar"]).cuda())
+    rt = [torch.zeros(b, hkv, dtype=torch.int32, device="cuda"), torch.full((b, hkv, T), -1, dtype=torch.int32, device="cuda"),
+          torch.full((b, hkv, T), NAN, device="cuda"), torch.full((b, hkv, (T + 31) // 32), -1, dtype=torch.int32, device="cuda")]
+    st.route = D.route_out(*rt)
+    n = max(lens)
+    st.fill(*(torch.from_numpy(x[k][:, :n]).to("cuda", torch.bfloat16) for k in "KV"), lens)
+    q = x["Q"][np.arange(b), np.asarray(lens) - 1]
+    st.decode(torch.from_numpy(q).to("cuda", torch.bfloat16))
+    counts, idx, bias, mask = (t.cpu().numpy() for t in rt)
+    _, ref = oracle.decode(q, x["K"], x["V"], x["qbar"], lens, chunk=B, alpha=alpha, gamma=gamma, inv_sigma=inv_sigma,
+                           want_route=True)
+    pos = (np.asarray(lens) - 1).reshape(b, 1)
+    sets = {(i, r, 0): idx[i, r, :counts[i, r]] for i in range(b) for r in range(hkv)}
+    mism, _ = check_routes(sets, ref, B, pos, T)
+    for (i, r, _), got in sets.items():
+        bits = ((mask[i, r].view(np.uint32)[:, None] >> np.arange(32, dtype=np.uint32)) & 1).reshape(-1)
+        assert np.array_equal(np.flatnonzero(bits), got)
+        if (i, r, 0) in mism or not len(got):
+            continue
+        w, margin = ref["w"][i, r, 0, got], ref["margin"][i, r, 0, got]
+        want = (np.log(w) - np.log(w).mean()) * inv_sigma
+        assert (np.abs(bias[i, r, :len(got)] - want) <= bias_tolerance(margin, alpha, gamma, inv_sigma)).all(), (i, r)
+    assert len(mism) <= 1
