@@ -141,59 +141,99 @@ __global__ void __launch_bounds__(kPlan) plan_copy_kernel(PageTab t, const int* 
     if (threadIdx.x == 0) { plan->pairs = code ? 0 : n; plan->ok = !code; }
 }
 
-// reserve: a warp per row counts the slots it lacks; then, if there are enough free pages, fills them.
+// reserve: the slots that the rows are to have (from the one that holds the next token on) form one list,
+// in the order of rows and slots; those without a page get the lowest free pages, if there are enough.
 __global__ void __launch_bounds__(kPlan) reserve_kernel(PageTab t, const int* counts, int count, int* status, PagesWs w)
 {
+    __shared__ int ends[kMarks], begins[kMarks];
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned first = free_mask(t.refs, t.num_pages, 0);
+    // slots of the rows up to and including b; the first of them in b's table row
+    int *end = t.batch <= kMarks ? ends : w.row, *begin = t.batch <= kMarks ? begins : w.own;
     unsigned bad = 0;
-    auto slots = [&](int b, int* s0, int* s1) {
-        const int L = t.seqlens[b], add = counts ? counts[b] : count;
-        *s0 = *s1 = 0;
-        if (add <= 0) return;
-        const long long end = (long long)L + add;
-        if (L < 0 || end > (long long)t.max_pages * t.page_size) { bad |= 1u << DASH_PAGES_LENGTH; return; }
-        *s0 = L / t.page_size;
-        *s1 = (int)((end + t.page_size - 1) / t.page_size);
-    };
-    for (int b = warp; b < t.batch; b += kPlan / 32) {
-        int s0, s1, n = 0;
-        slots(b, &s0, &s1);
-        for (int k = s0; k < s1; k += 32)
-            n += __popc(__ballot_sync(0xffffffffu, k + lane < s1 && t.page_table[(long long)b * t.max_pages + k + lane] < 0));
-        if (lane == 0) w.row[b] = n;
-    }
-    if (first_failure(bad, status)) return;
-    int want = 0;
+    int width = 0;
     for (int b0 = 0; b0 < t.batch; b0 += kPlan) {
-        const int b = b0 + threadIdx.x, n = b < t.batch ? w.row[b] : 0;
-        int total;
+        const int b = b0 + threadIdx.x, add = b < t.batch ? (counts ? counts[b] : count) : 0;
+        int n = 0, from = 0, total;
+        if (add > 0) {
+            const int L = t.seqlens[b];
+            const long long to = (long long)L + add;
+            if (L < 0 || to > (long long)t.max_pages * t.page_size) bad |= 1u << DASH_PAGES_LENGTH;
+            else {
+                from = L / t.page_size;
+                n = (int)((to + t.page_size - 1) / t.page_size) - from;
+            }
+        }
         const int at = block_scan(n, &total);
-        if (b < t.batch) w.row[b] = want + at;   // pages given to the rows before
+        if (b < t.batch) {
+            end[b] = width + at + n;
+            begin[b] = from;
+        }
+        width += total;
+    }
+    if (first_failure(bad, status)) return;   // (a barrier: `end` is there)
+    // one slot per thread where they are enough, else kPer consecutive ones per thread and step
+    const int per = width <= kPlan ? 1 : kPer;
+    int* at[kPer];   // the table entries behind this thread's slots
+    auto lacking = [&](int i0) {   // bit k: slot k of this thread has no page
+        const int i = i0 + (int)threadIdx.x * per;
+        if (i >= width) return 0u;
+        int l = 0, h = t.batch - 1;   // the row with end[l - 1] <= i < end[l]
+        while (l < h) {
+            const int m = (l + h) >> 1;
+            if (end[m] <= i) l = m + 1;
+            else h = m;
+        }
+        int* e = t.page_table + (long long)l * t.max_pages + begin[l] + (i - (l ? end[l - 1] : 0));
+        at[0] = e;
+        if (per == 1) return *e < 0 ? 1u : 0u;
+#pragma unroll
+        for (int k = 1; k < kPer; ++k) {
+            ++e;
+            if (i + k < width && i + k == end[l]) {   // on to the next row with slots
+                do ++l;
+                while (end[l] <= i + k);
+                e = t.page_table + (long long)l * t.max_pages + begin[l];
+            }
+            at[k] = e;
+        }
+        int v[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) v[k] = *(i + k < width ? at[k] : at[0]);
+        unsigned m = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+            if (i + k < width && v[k] < 0) m |= 1u << k;
+        return m;
+    };
+    const unsigned m0 = lacking(0);
+    int want;
+    block_scan(__popc(m0), &want);
+    for (int i0 = kPlan * per; i0 < width; i0 += kPlan * per) {
+        int total;
+        block_scan(__popc(lacking(i0)), &total);
         want += total;
     }
-    __syncthreads();
     if (want == 0) return;
     if (want > t.num_pages || lowest_free(t.refs, t.num_pages, want, w.dst, first) < want) {
         if (threadIdx.x == 0) fail(status, DASH_PAGES_FULL);
         return;
     }
-    for (int b = warp; b < t.batch; b += kPlan / 32) {
-        int s0, s1, at = w.row[b];
-        slots(b, &s0, &s1);
-        for (int k = s0; k < s1; k += 32) {
-            int* e = t.page_table + (long long)b * t.max_pages + k + lane;
-            const bool on = k + lane < s1 && *e < 0;
-            const unsigned m = __ballot_sync(0xffffffffu, on);
-            if (on) {
-                const int pg = w.dst[at + __popc(m & ((1u << lane) - 1u))];
-                *e = pg;
+    int done = 0;
+    for (int i0 = 0; i0 < width; i0 += kPlan * per) {
+        // (with several steps `at` is another step's by now)
+        const unsigned m = width <= kPlan * per ? m0 : lacking(i0);
+        int total;
+        int j = done + block_scan(__popc(m), &total);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+            if (m >> k & 1) {
+                const int pg = w.dst[j++];
+                *at[k] = pg;
                 t.refs[pg] = 1;
             }
-            at += __popc(m);
-        }
+        done += total;
     }
 }
 
@@ -259,8 +299,10 @@ __global__ void __launch_bounds__(kPlan) plan_compact_kernel(PageTab t, int* use
     pdl_wait();
     pdl_launch_dependents();
     Plan* plan = reinterpret_cast<Plan*>(w.head);
-    int U = 0;
-    for (int p = threadIdx.x; p < t.num_pages; p += kPlan) U += t.refs[p] > 0;
+    const unsigned first = free_mask(t.refs, t.num_pages, 0);   // of the first step's pages
+    const int here = max(0, min(kPer, t.num_pages - (int)threadIdx.x * kPer));
+    int U = here - __popc(first);
+    for (int p = kPlan * kPer + threadIdx.x; p < t.num_pages; p += kPlan) U += t.refs[p] != 0;
     {
         int total;
         block_scan(U, &total);
@@ -269,11 +311,12 @@ __global__ void __launch_bounds__(kPlan) plan_compact_kernel(PageTab t, int* use
     int holes = 0, movers = 0;
     for (int p0 = 0; p0 < t.num_pages; p0 += kPlan * kPer) {
         const int p = p0 + threadIdx.x * kPer;
+        const unsigned none = p0 ? free_mask(t.refs, t.num_pages, p0) : first;
         unsigned h = 0, m = 0;
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
             if (p + k >= t.num_pages) continue;
-            const bool on = t.refs[p + k] > 0;
+            const bool on = !(none >> k & 1);
             if (p + k < U && !on) h |= 1u << k;
             if (p + k >= U && on) m |= 1u << k;
             if (p + k >= U && !on) w.mark[p + k] = p + k;   // table entries of pages without a count stay
