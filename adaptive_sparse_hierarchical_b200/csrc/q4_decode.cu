@@ -183,23 +183,24 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
         const int total = scan(pre, [&](int x) { return pre[x + 1]; }), nb = (int)gridDim.x;
         // every warp of a block in use has a granule
         int used = min(nb, (total + W - 1) / W), x = 0;
-        long long lo = (long long)total * blockIdx.x / max(used, 1), hi = (long long)total * (blockIdx.x + 1) / max(used, 1);
+        const int share = total / max(used, 1), more = total - share * used, blk = (int)blockIdx.x;
+        int lo = blk * share + min(blk, more), hi = lo + share + (blk < more);
         // Where one round of a block's warps is enough, pairs get blocks of their own: a pair that starts
         // inside a block costs it a merge, a descriptor chase and an empty ring (three short sequences: 17.4
         // us so, 18.9 with even shares; with more rounds even shares are as good or better).
         if (BR <= nb && total <= nb * W && scan(first_blk, [&](int x) { return (pre[x + 1] - pre[x] + W - 1) / W; }) <= nb) {
             used = first_blk[BR];
-            if ((int)blockIdx.x < used) {
-                x = last_le(first_blk, blockIdx.x);
-                lo = pre[x] + ((int)blockIdx.x - first_blk[x]) * W;
-                hi = min((int)lo + W, pre[x + 1]);
+            if (blk < used) {
+                x = last_le(first_blk, blk);
+                lo = pre[x] + (blk - first_blk[x]) * W;
+                hi = min(lo + W, pre[x + 1]);
             }
-        } else if ((int)blockIdx.x < used) {
-            x = last_le(pre, (int)lo);
+        } else if (blk < used) {
+            x = last_le(pre, lo);
         }
         if (lane == 0) {
-            range[0] = (int)lo;
-            range[1] = (int)blockIdx.x < used ? (int)hi : 0;
+            range[0] = lo;
+            range[1] = blk < used ? hi : 0;
             range[2] = x;
         }
     }
@@ -300,6 +301,16 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
             }
             cp_async_commit();
         };
+        uint4 raw[NT][NG];   // the query: this lane's eight elements of each scale group, heads 8 nt + g
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int gg = 0; gg < NG; ++gg) {
+                raw[nt][gg] = make_uint4(0u, 0u, 0u, 0u);
+                if (nt * 8 + g < G)
+                    raw[nt][gg] = *reinterpret_cast<const uint4*>(
+                        a.q + ((long long)b * s.hq + r * G + nt * 8 + g) * D + gg * kGrp + t4 * 8);
+            }
         fetch(0);
         publish(0);
 #pragma unroll
@@ -311,16 +322,12 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
         float fac[NT][2];         // logit per accumulated unit of heads 2 t4 and 2 t4 + 1
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int h = nt * 8 + g;
-            uint4 raw[NG];
             uint32_t top = 0;
 #pragma unroll
             for (int gg = 0; gg < NG; ++gg) {
-                raw[gg] = make_uint4(0u, 0u, 0u, 0u);
-                if (h < G)
-                    raw[gg] = *reinterpret_cast<const uint4*>(a.q + ((long long)b * s.hq + r * G + h) * D + gg * kGrp + t4 * 8);
-                top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[gg].x & 0x7fff7fffu, raw[gg].y & 0x7fff7fffu),
-                                             __vmaxu2(raw[gg].z & 0x7fff7fffu, raw[gg].w & 0x7fff7fffu)));
+                const uint4 w = raw[nt][gg];
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                             __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
             }
             top = max(top & 0xffffu, top >> 16);
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -335,7 +342,7 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
 #pragma unroll
             for (int gg = 0; gg < NG; ++gg) {
                 float v[8];
-                Vec<__nv_bfloat16>::cvt(raw[gg], v);
+                Vec<__nv_bfloat16>::cvt(raw[nt][gg], v);
                 sum[gg] = 0.f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum[gg] += v[e] * up;
