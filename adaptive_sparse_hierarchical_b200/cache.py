@@ -8,6 +8,7 @@ import torch
 from . import _lib as L
 from .api import _st
 
+
 def _current(index):
     """Raw handle of device `index`'s current stream."""
     return torch._C._cuda_getCurrentRawStream(index)
@@ -36,6 +37,13 @@ def _need(t, name, device, dtype, shape=None):
     return t
 
 
+def _int32(v, name):
+    """A number that a C int holds (anything else would be cut down silently)."""
+    if not -2**31 <= v < 2**31:
+        raise ValueError(f"{name}: {v} does not fit 32 bits")
+    return v
+
+
 def _signature(t):
     """What the checks of an argument depend on."""
     return (t.shape, t.stride(), t.dtype, t.device) if isinstance(t, torch.Tensor) else type(t)
@@ -50,7 +58,8 @@ class Q4DecodeState:
     k_exp, v_exp: power-of-two exponents of the data's size (scales cover 2^-9 .. 448 times 2^exp).
     page_table (device int32 [batch, max_pages]) may be rewritten between steps, by the caller or by
     a PagePool; without one, sequence b owns pages b * max_pages and on.  Copying the tensors saves
-    or restores a session."""
+    or restores a session.  Calls share the cache's workspace and output, so they go to one stream at
+    a time (graphs of one cache are replayed one after another)."""
 
     def __init__(self, batch, capacity, h_q, h_kv, d, *, chunk, alpha, gamma, page_size, num_pages=None,
                  page_table=None, k_exp=0, v_exp=0, inv_sigma=1.0, device="cuda", qbar=None):
@@ -157,7 +166,7 @@ class Q4DecodeState:
         p, m = self._check("load", K, V, rows, "start")
         if m != n:
             raise ValueError(f"K and V must hold {n} tokens")
-        rc = self._lib.dash_load_q4(p, self.kv, None if rows is None else rows.data_ptr(), 0 if rows is not None else start, n,
+        rc = self._lib.dash_load_q4(p, self.kv, None if rows is None else rows.data_ptr(), 0 if rows is not None else _int32(start, "start"), n,
                                     self.seqlens.data_ptr(), K.data_ptr(), V.data_ptr(), _current(self._index))
         if rc:
             L._check(rc, "dash_load_q4")
@@ -195,6 +204,9 @@ class Q4DecodeState:
                 self.step(*self._ins)
             return out
         for mine, t in zip(self._ins, (q, k_new, v_new)):
+            if t.shape != mine.shape or t.dtype != mine.dtype:
+                raise ValueError(f"the graph was recorded for {mine.dtype} {tuple(mine.shape)}")
+        for mine, t in zip(self._ins, (q, k_new, v_new)):
             mine.copy_(t)
         self._graph.replay()
         return self.O
@@ -206,7 +218,8 @@ class PagePool:
     device int32 tensors that are changed in place.  add() registers what pages and rows hold; every
     operation is enqueued on the current stream (or `stream`) and works on the device alone, so it can
     be captured into a CUDA graph.  A request that cannot be met changes nothing and leaves its reason
-    in `status`, which check() raises."""
+    in `status`, which check() raises.  Operations share the pool's workspace and tables, so they go to
+    one stream at a time."""
 
     REASONS = {1: "an index is outside its range, or a page is missing", 2: "a destination occurs twice or is also a source",
                3: "a destination row is not empty", 4: "not enough free pages", 5: "a length is beyond the row's pages"}
@@ -338,7 +351,7 @@ class PagePool:
             per = self._list(count, "count")
             if per.shape != self.seqlens.shape:
                 raise ValueError("count: one number per row is needed")
-        rc = self._lib.dash_pages_reserve(self.pg, None if per is None else per.data_ptr(), 0 if per is not None else count,
+        rc = self._lib.dash_pages_reserve(self.pg, None if per is None else per.data_ptr(), 0 if per is not None else _int32(count, "count"),
                                           self.status.data_ptr(), *self._ws, _current(self._index))
         if rc:
             L._check(rc, "dash_pages_reserve")

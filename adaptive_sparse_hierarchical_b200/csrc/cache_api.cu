@@ -29,6 +29,8 @@ bool on(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 
 int status_of(cudaError_t e) { return e == cudaSuccess ? DASH_OK : DASH_ELAUNCH; }
 
 constexpr int kMaxGridYZ = 65535;
+// Sizes of page and row arrays: the movers number 8 KB pieces of a page, and of a row's run, in 32 bits.
+constexpr long long kMaxPageBytes = 1ll << 36, kMaxRunBytes = 1ll << 42;
 
 int check_q4(const dash_params* p, const dash_q4_kv* kv)
 {
@@ -107,19 +109,24 @@ int check_pages(const dash_pages* pg)
     if (!pg->page_table || !pg->refs || !pg->seqlens) return DASH_EINVAL;
     if (!on(pg->page_table, 4) || !on(pg->refs, 4) || !on(pg->seqlens, 4)) return DASH_EALIGN;
     if ((long long)pg->max_pages * pg->page_size > 0x7fffffffll) return DASH_EINVAL;
+    // the table's slots are numbered in 32 bits, its rows' parts are the y blocks of a launch
+    if ((long long)pg->max_pages * pg->batch > 1ll << 30 || pg->max_pages > 1 << 25) return DASH_EUNSUPPORTED;
     if (pg->num_arrays < 0 || pg->num_rows < 0 || (pg->num_arrays && !pg->arrays) || (pg->num_rows && !pg->rows))
         return DASH_EINVAL;
     for (int i = 0; i < pg->num_arrays; ++i) {
         const dash_page_array& a = pg->arrays[i];
-        if (!a.data || a.page_bytes < 0 || a.page_stride < a.page_bytes || a.page_bytes > (1ll << 40)) return DASH_EINVAL;
+        if (!a.data || a.page_bytes < 0 || a.page_stride < a.page_bytes) return DASH_EINVAL;
+        if (a.page_bytes > kMaxPageBytes) return DASH_EUNSUPPORTED;
         if (!on(a.data, 16) || a.page_bytes % 16 || a.page_stride % 16) return DASH_EALIGN;
     }
     for (int i = 0; i < pg->num_rows; ++i) {
         const dash_row_array& r = pg->rows[i];
         if (!r.data || r.unit_bytes < 0 || r.heads < 0 || r.max_units < 0 || r.unit_tokens < 0 ||
-            r.unit_bytes > (1ll << 40) || r.row_stride < 0 || r.head_stride < 0 || r.clear < DASH_ROW_KEPT ||
-            r.clear > DASH_ROW_STATE)
+            r.row_stride < 0 || r.head_stride < 0 || r.clear < DASH_ROW_KEPT || r.clear > DASH_ROW_STATE)
             return DASH_EINVAL;
+        if (r.unit_bytes > kMaxRunBytes / (r.max_units ? r.max_units : 1) ||
+            r.head_stride > (1ll << 62) / (r.heads ? r.heads : 1) - kMaxRunBytes)
+            return DASH_EUNSUPPORTED;
         if (!on(r.data, 4) || (r.unit_bytes | r.row_stride | r.head_stride) % 4) return DASH_EALIGN;
         // a row's runs must not reach into each other or into the next row
         const long long run = r.unit_bytes * r.max_units;
@@ -155,7 +162,9 @@ int dash_append_q4(const dash_params* p, const dash_q4_kv* kv, const void* K_new
 {
     const int rc = check_q4(p, kv);
     if (rc != DASH_OK) return rc;
-    if (n_new < 0 || (n_new && (!K_new || !V_new)) || !qbar || !kbar_cache || !partial_state || !seqlens) return DASH_EINVAL;
+    if (n_new < 0 || (n_new && (!K_new || !V_new)) || !qbar || !partial_state || !seqlens) return DASH_EINVAL;
+    if (!kbar_cache && p->seqlen >= p->chunk) return DASH_EINVAL;   // (shorter caches have no summaries)
+    if (n_new > p->seqlen) n_new = p->seqlen;                       // the others would be dropped
     if (!on(K_new, 16) || !on(V_new, 16) || !rows_ok(p->k_strides) || !rows_ok(p->v_strides)) return DASH_EALIGN;
     if (!on(qbar, 4) || !on(kbar_cache, 4) || !on(partial_state, 4) || !on(seqlens, 4) || !on(counts, 4)) return DASH_EALIGN;
     if (n_new == 0) return DASH_OK;
@@ -182,11 +191,14 @@ int dash_decode_q4(const dash_params* p, const dash_q4_kv* kv, const void* q, co
 {
     int rc = check_q4(p, kv);
     if (rc != DASH_OK) return rc;
-    const bool dense = p->gamma == 0.f, routed = !dense || route;
+    // a cache shorter than a chunk has nothing to route
+    const bool none = p->seqlen < p->chunk, dense = p->gamma == 0.f || none, routed = !none && (!dense || route);
     if (!q || !seqlens || !O || (routed && !kbar_cache)) return DASH_EINVAL;
     if (!on(q, 16) || !on(O, 16) || !on(kbar_cache, 16) || !on(seqlens, 4)) return DASH_EALIGN;
     if ((long long)p->batch * p->h_kv > q4_max_pairs()) return DASH_EUNSUPPORTED;
     const Shape s = shape_of(p);
+    // the pairs' granules (16 tokens or more) are numbered in 32 bits
+    if ((long long)p->batch * p->h_kv * (p->seqlen / 16 + 1ll) > 0x7fffffffll) return DASH_EUNSUPPORTED;
     // Stage 1 keeps every head's logits of one (sequence, KV head) in shared memory
     if (routed && (size_t)s.g * (size_t)s.T * 4 > 225 * 1024) return DASH_EUNSUPPORTED;
     const Q4Layout L = q4_layout(p);
@@ -208,6 +220,10 @@ int dash_decode_q4(const dash_params* p, const dash_q4_kv* kv, const void* q, co
                            ? launch_route_q4(s, q, kbar_cache, seqlens, rt, X, err, (cudaStream_t)stream)
                            : launch_route_decode(s, p->dtype, q, kbar_cache, s.T, seqlens, rt, X, err, (cudaStream_t)stream));
         if (rc != DASH_OK) return rc;
+    }
+    if (none && route) {
+        const size_t bh = (size_t)p->batch * p->h_kv;
+        if ((rc = status_of(cudaMemsetAsync(rt.counts, 0, bh * 4, (cudaStream_t)stream))) != DASH_OK) return rc;
     }
     return status_of(launch_attend_q4(s, cache_of(kv), q, seqlens, rt, dense, (float*)(ws + L.part), (int*)(ws + L.span), O,
                                       (cudaStream_t)stream));

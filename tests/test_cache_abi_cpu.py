@@ -99,6 +99,14 @@ def test_bad_calls():
     assert dec(p=_p(**big), kv=_kv(max_pages=1024), n=1 << 50) == L.DASH_EUNSUPPORTED
     assert dec(p=_p(**big, gamma=0.0), kv=_kv(max_pages=1024), kb=None, n=16) == L.DASH_EWORKSPACE
     assert dec(p=_p(gamma=0.0), kb=None, r=L.route_out(256), n=1 << 50) == L.DASH_EINVAL   # routes asked for
+    # more granules than 32 bits number: 2048 pairs of 2^25 tokens
+    huge = _p(batch=1024, seqlen=1 << 25, chunk=128, gamma=0.0)
+    assert dec(p=huge, kv=_kv(max_pages=1 << 18), kb=None, n=1 << 60) == L.DASH_EUNSUPPORTED
+    # a cache shorter than a chunk has no summaries to point to: only the workspace is missed here
+    short = dict(p=_p(seqlen=63), kb=None)
+    assert dec(**short, n=16) == L.DASH_EWORKSPACE
+    assert append(**short, n=0) == L.DASH_OK
+    assert append(p=_p(seqlen=64), kb=None, n=0) == L.DASH_EINVAL
 
 
 def _pg(arrays=(), rows=(), **kw):
@@ -122,6 +130,11 @@ A, W = L.dash_page_array, L.dash_row_array
     (_pg(rows=[W(256, 64, 16, 16, 2, 2, 0, 0)]), L.DASH_EINVAL),    # runs overlap
     (_pg(rows=[W(256, 32, 32, 16, 2, 2, 32, 0)]), L.DASH_EINVAL),   # rows overlap
     (_pg(rows=[W(256, 64, 16, 16, -1, 1, 0, 0)]), L.DASH_EINVAL), (_pg(rows=[W(256, 64, 16, 16, 2, 1, 0, 3)]), L.DASH_EINVAL),
+    # sizes whose pieces or slots 32 bits do not number
+    (_pg([A(256, 1 << 37, 1 << 37)]), L.DASH_EUNSUPPORTED), (_pg(batch=1 << 20, max_pages=1 << 11), L.DASH_EUNSUPPORTED),
+    (_pg(batch=1, max_pages=1 << 26, page_size=16), L.DASH_EUNSUPPORTED),
+    (_pg(rows=[W(256, 1 << 50, 1 << 50, 1 << 40, 1, 8, 0, 0)]), L.DASH_EUNSUPPORTED),
+    (_pg(rows=[W(256, 1 << 62, 1 << 61, 64, 4, 1, 0, 0)]), L.DASH_EUNSUPPORTED),
 ])
 def test_bad_pages(pg, code):
     lib, ws = D.load(), 1 << 40

@@ -401,6 +401,8 @@ def test_refused_registrations():
         pool.free(torch.tensor([1], device="cuda"))
     with pytest.raises(ValueError):
         pool.fork([0, 1], [2])
+    with pytest.raises(ValueError):
+        pool.reserve((1 << 32) + 1)
     pool.free([0])
     pool.check()
 

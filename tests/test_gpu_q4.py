@@ -391,6 +391,42 @@ def test_steps_graph_and_streams():
         assert torch.equal(getattr(eager, name), getattr(other, name)), name
 
 
+def test_graph_refuses_other_shapes():
+    """A recorded step takes the sizes and type it was recorded with: nothing is broadcast or converted."""
+    rng = np.random.default_rng(28)
+    st = _state(rng, 2, 128, 4, 2, 64, chunk=32, page=32)
+    q, k = _bf16(rng, 2, 4, 64).cuda(), _bf16(rng, 2, 2, 64).cuda()
+    st.graph_step(q, k, k)
+    before = st.graph_step(q, k, k).clone()
+    for bad in ((q[:1], k, k), (q, k[:1], k), (q, k, k.float()), (q, k, k[:, :, :1])):
+        with pytest.raises(ValueError):
+            st.graph_step(*bad)
+    assert st.seqlens.tolist() == [2, 2] and torch.equal(st.O, before)
+
+
+def test_cache_shorter_than_a_chunk():
+    """No chunk ever completes: no summaries, and routed attention is attention over the own chunk."""
+    rng = np.random.default_rng(29)
+    cap, n, hq, hkv, d = 20, 17, 4, 2, 64
+    K, V, q = _bf16(rng, 2, n, hkv, d), _bf16(rng, 2, n, hkv, d), _bf16(rng, 2, hq, d)
+    out = []
+    for gamma in (3.0, 0.0):
+        st = _state(np.random.default_rng(30), 2, cap, hq, hkv, d, chunk=32, page=32, gamma=gamma)
+        st.fill(K[:, :n - 1].cuda(), V[:, :n - 1].cuda(), [n - 1, 0])
+        counts = torch.full((2, hkv), 7, dtype=torch.int32, device="cuda")
+        st.route = D.route_out(counts)
+        st.append(K[:, n - 1].cuda(), V[:, n - 1].cuda())
+        out.append(st.decode(q.cuda()).clone())
+        assert not counts.any() and st.seqlens.tolist() == [n, 1]
+        for i, m in enumerate((n, 1)):
+            _check_pools(st, i, K[i, n - m:].double().numpy(), V[i, n - m:].double().numpy())
+    ref, err = _decode_ref(st, q.double().numpy(), np.stack([K[0].double().numpy(), np.roll(K[1].double().numpy(), 1, 0)]),
+                           np.stack([V[0].double().numpy(), np.roll(V[1].double().numpy(), 1, 0)]), [n, 1], hq, hkv, d, 32,
+                           None, 0, 0)
+    _check_out(out[0], ref, err)
+    assert torch.equal(*out)
+
+
 def test_matches_bf16_cache_routes():
     """The 4-bit cache routes as the bf16 paged cache does (same summaries), step after step, and its outputs stay
     within the quantisation's distance."""
@@ -511,7 +547,7 @@ def test_refusals():
         with pytest.raises((TypeError, ValueError)):
             bad()
     for bad in (lambda: st.append(k, k[:, :2]), lambda: st.append(k[:1], k[:1]), lambda: st.append(k, k, ints(1)),
-                lambda: st.append(k.transpose(2, 3), k.transpose(2, 3)), lambda: st.append(k, k, ints(1, 0, 2, 0)[::2]),
+                lambda: st.append(k.transpose(2, 3), k.transpose(2, 3)), lambda: st.append(k, k, ints(1, 0, 2, 0)[::2]), lambda: st.load(1 << 32, 3), lambda: st.load(-(1 << 31) - 1, 3),
                 lambda: st.load(ints(0), 3), lambda: st.load(0, 3, k[:, :2], k), lambda: st.decode(torch.zeros_like(st.O).transpose(0, 1))):
         with pytest.raises(ValueError):
             bad()
