@@ -13,6 +13,10 @@
 //      registers: a Newton step is one pass over registers and one block barrier.  The heads' weights take the
 //      logits' place (in L2: reading them from the other blocks' shared memory took twice as long), and block
 //      k adds them up for the k-th quarter of the chunks.
+// Measured with cold caches for 16 pairs of 2047 chunks and 16 heads of 128: logits 10.2 us (16.8 MB, 1.7 TB/s:
+// a read of this size is latency), the rest 14.7 (five Newton steps of about 1 us, two passes through L2, three
+// cluster barriers); one cluster for everything takes 25 to 26 us there, and 2 us more than these two
+// together when a step follows another (a whole routed call 66 -> 62 us).  Clusters of 8 are slower: 15 of 16 fit.
 #include <cooperative_groups.h>
 
 #include "entmax.cuh"
