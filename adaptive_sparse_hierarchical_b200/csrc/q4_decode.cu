@@ -20,12 +20,16 @@
 //      exact in f16 (its elements for the upper masks divided by 16) down to 2^-27 of the largest.
 //      Each scale group's sum is multiplied by the key's scale in fp32.  The codes' offset of 8 is one
 //      more MMA: the tokens' scales times -8 sum(q) of each group (two f16 numbers, 22 bits).
-//   V: the operand needs the scale inside the sum over tokens.  1024 + u (or 1024 + 16 u) in f16,
-//      one f16x2 fma (1024 + u) s' - 1032 s' gives (u - 8) s' exactly: with s' = scale / 16,
-//      1032 s' has at most 8 + 4 - 1 = 11 significant bits (129 * 15 < 2^11) and is below 2^15.
-//   P is rounded to f16 (2^-12 relative; sums of P are taken before the rounding, in fp32) and
-//   turned from S^T's accumulator layout into an operand by movmatrix.
-// The reference of the softmax moves only when a logit exceeds it by more than 6 (P <= 64 in f16).
+//   V: ldmatrix turns the rows: a register holds the codes 4 g .. 4 g + 3 of a group for two tokens, and masks
+//      and one byte permutation make four operands u_0, u_0 + 16 u_1, u_2, u_2 + 16 u_3 of it (subnormals again;
+//      the difference of a pair's sums is taken at the end).  The 16 rows of a tile belong to one scale group, so
+//      the scale goes to the other side: P s in f16, one product per group, token pair and head.  The offset is
+//      8 times the sum of P s, kept by one more MMA for two groups (A = the scales, B = P).
+//   P is rounded to f16 (2^-12 relative; sums of P are taken before the rounding, in fp32), turned from S^T's
+//   accumulator layout into an operand by movmatrix, and P s is rounded to f16 once more (2^-12, of terms with codes
+//   up to 15).  P is 2^room at the reference, and both P and P s stay below 2^15: room is 9 while the value scales
+//   met so far are below 1/2, less for larger ones (0 from 256 on), so small scales do not push P s below f16's
+//   normals.  The reference moves only when a logit exceeds it by more than 6, or when room shrinks.
 //
 // Bound: 17/32 bytes of HBM per element are few enough for the unpacking to count: per 16 tokens of 128
 // elements a warp issues about 70 mask, conversion and fp32 instructions for K, 95 for V, 17 MMAs per 8 heads, the softmax.
@@ -36,8 +40,6 @@
 // second pair of a block.  Three sequences of 777 tokens and fewer: 16.5 us in four launches.
 #include <cuda_fp16.h>
 
-#include <type_traits>
-
 #include "q4.cuh"
 #include "stage2_mma.cuh"
 
@@ -45,7 +47,6 @@ namespace dash {
 namespace {
 
 constexpr int kMaxPairs = 2048;
-constexpr int kMaxBlocks = 2048;
 constexpr int kMeta = 64;         // granule descriptors per warp (two halves of 32)
 
 // Descriptor of a granule: where its codes and scales lie, its chunk's bias, tokens | mapped << 8.
@@ -85,24 +86,14 @@ __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void prefetch_l2(const char* p) { asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p)); }
 __device__ __forceinline__ uint32_t h2(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
 __device__ __forceinline__ __half2 h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
-// f(512), f(1024), ... below END, as constants
-template <int OFF, int END, typename F>
-__device__ __forceinline__ void each512(const F& f)
+// d = a b, k = 8
+__device__ __forceinline__ void mma_f16_k8(float* d, uint32_t a0, uint32_t a1, uint32_t b)
 {
-    if constexpr (OFF < END) {
-        f(std::integral_constant<int, OFF>());
-        each512<OFF + 512, END>(f);
-    }
-}
-// (x & MASK) | magic in one instruction (written in C with two constants it becomes two)
-template <uint32_t MASK>
-__device__ __forceinline__ __half2 pick(uint32_t x, uint32_t magic)
-{
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "n"(MASK), "r"(magic));
-    return h2(r);
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};\n"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]) : "r"(a0), "r"(a1), "r"(b), "f"(0.f));
 }
 // d = a b
 __device__ __forceinline__ void mma_f16_0(float* d, const uint32_t* a, uint32_t b0, uint32_t b1)
@@ -111,6 +102,19 @@ __device__ __forceinline__ void mma_f16_0(float* d, const uint32_t* a, uint32_t 
                  "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// (c0, c1) + a (b0, b1) in one instruction
+__device__ __forceinline__ void fma2(float& c0, float& c1, float a, float b0, float b1)
+{
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %2};\n\tmov.b64 b, {%3, %4};\n\tmov.b64 c, {%0, %1};\n\t"
+        "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}\n"
+        : "+f"(c0), "+f"(c1)
+        : "f"(a), "f"(b0), "f"(b1));
+}
+// Four e4m3 bytes as two f16x2
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t four, uint32_t& a, uint32_t& b)
+{
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}\n" : "=r"(a), "=r"(b) : "r"(four));
 }
 __device__ __forceinline__ float ex2(float x)
 {
@@ -129,27 +133,27 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-// Token (row of 16 tokens) behind row m < 8 of S^T (row m + 8: the same + 8).  Even rows 0..3 and
-// odd rows 5, 4, 7, 6: keys read two rows of opposite parity at once, values rows 0..3 or 4..7,
-// which the swizzle of the value rows spreads over all banks.
-__device__ __forceinline__ int tok_of(int m) { return (m & 1) ? ((m >> 1) ^ 1) + 4 : m >> 1; }
-
 // Length of sequence b as the kernels use it.
 __device__ __forceinline__ int len_of(const Shape& s, const int* seqlens, int b) { return min(max(seqlens[b], 0), s.n); }
 
 template <int D, int NT, int U>
 __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_kernel(Shape s, Q4 c, Routes rt, Attend a)
 {
-    constexpr int W = Cfg<NT>::W, NG = D / kGrp, NW = D / 64, MT = D / 16;
+    constexpr int W = Cfg<NT>::W, NG = D / kGrp, MT = D / 16;
     using St = Stage<D, U>;
     constexpr int OLD = St::OLD, kGran = St::GRAN, kStages = St::N;
     static_assert(8 * NT * OLD * 4 <= kStages * St::BYTES, "the merge buffer reuses a warp's ring");
     extern __shared__ __align__(128) char smem[];
-    __shared__ int pre[kMaxPairs + 1], first_blk[kMaxBlocks + 1], range[3];
+    __shared__ int pre[kMaxPairs + 1], at[kMaxPairs + 1], range[3];
     __shared__ float mrg_m[W][8 * NT], mrg_l[W][8 * NT], mrg_s[W][8 * NT], tot_m[8 * NT], tot_l[8 * NT];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int BR = s.batch * s.hkv, G = s.g, NB = s.B / kGran;
+    {   // the page table and the query on their way to L2 while the routing still runs
+        const long long at = ((long long)blockIdx.x * (32 * W) + threadIdx.x) * 128;
+        if (at < (long long)s.batch * c.pmax * 4) prefetch_l2((const char*)c.pt + at);
+        if (at < (long long)s.batch * s.hq * D * 2) prefetch_l2((const char*)a.q + at);
+    }
     pdl_wait();   // the routes and the appended tokens of this step
     pdl_launch_dependents();
     for (int x = threadIdx.x; x < BR; x += 32 * W) {
@@ -187,21 +191,29 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
         };
         const int total = scan(pre, [&](int x) { return pre[x + 1]; }), nb = (int)gridDim.x;
         // every warp of a block in use has a granule
-        int used = min(nb, (total + W - 1) / W), x = 0;
-        const int share = total / max(used, 1), more = total - share * used, blk = (int)blockIdx.x;
-        int lo = blk * share + min(blk, more), hi = lo + share + (blk < more);
+        int used = min(nb, (total + W - 1) / W), x = 0, lo = 0, hi = 0;
+        const int blk = (int)blockIdx.x;
         // Where one round of a block's warps is enough, pairs get blocks of their own: a pair that starts
         // inside a block costs it a merge, a descriptor chase and an empty ring (three short sequences: 17.4
         // us so, 18.9 with even shares; with more rounds even shares are as good or better).
-        if (BR <= nb && total <= nb * W && scan(first_blk, [&](int x) { return (pre[x + 1] - pre[x] + W - 1) / W; }) <= nb) {
-            used = first_blk[BR];
+        if (BR <= nb && total <= nb * W && scan(at, [&](int x) { return (pre[x + 1] - pre[x] + W - 1) / W; }) <= nb) {
+            used = at[BR];
             if (blk < used) {
-                x = last_le(first_blk, blk);
-                lo = pre[x] + (blk - first_blk[x]) * W;
+                x = last_le(at, blk);
+                lo = pre[x] + (blk - at[x]) * W;
                 hi = min(lo + W, pre[x + 1]);
             }
         } else if (blk < used) {
-            x = last_le(pre, lo);
+            // Even shares of the list, in which a pair starts with kPad granules that stand for that cost (four
+            // rounds; two to five measure alike, none costs 3 to 4 us in the two large cases above).
+            constexpr int kPad = 4 * W;
+            const int all = scan(at, [&](int x) { return pre[x + 1] > pre[x] ? pre[x + 1] - pre[x] + kPad : 0; });
+            const int share = all / used, more = all - share * used;
+            const int v0 = blk * share + min(blk, more), v1 = v0 + share + (blk < more);
+            auto place = [&](int v, int y) { return pre[y] + max(0, v - at[y] - kPad); };
+            x = last_le(at, v0);
+            lo = place(v0, x);
+            hi = place(v1, last_le(at, v1));
         }
         if (lane == 0) {
             range[0] = lo;
@@ -222,17 +234,15 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
     Meta& meta = *reinterpret_cast<Meta*>(smem + W * kStages * St::BYTES + warp * sizeof(Meta));
     // the operands carry the codes times 2^-24
     const float scale2 = kLog2e * rsqrtf((float)D) * exp2i(c.kexp) * 16777216.f;
-    const float out_scale = 16.f * exp2i(c.vexp);
-    uint32_t magic = 0x64006400u;                    // 1024, 1024 in f16
-    asm volatile("" : "+r"(magic));                  // kept in a register
-    const int tk = tok_of(g);                        // this lane's key rows: tk, tk + 8
-    const int vr0 = t4, vr1 = (t4 ^ 1) + 4;          // its value rows: vr0, vr1, vr0 + 8, vr1 + 8
-    // places of its words and scales in a stage (16-byte pieces of value rows are swizzled, see issue())
-    auto v_at = [&](int row) {
-        return St::V + (D == 128 ? row * 64 + ((g >> 1) ^ (((row >> 1) & 1) << 1)) * 16 + (g & 1) * 8 : row * 32 + g * 4);
+    const float out_scale = exp2i(24 + c.vexp);
+    // This lane's row of the 8 x 8 matrices of 16 bits that ldmatrix takes from the value rows: token
+    // (lane & 7) + 8 (lane >> 3 & 1), groups lane >> 4 and (D = 128) 2 more.  The groups of a row are
+    // swizzled so that eight tokens' pieces of one group lie in different banks.
+    auto v_at = [&](int group) {
+        const int tok = (lane & 7) + ((lane >> 3) & 1) * 8;
+        return (uint32_t)(St::V + tok * (D / 2) + (group ^ ((D == 128 ? tok >> 1 : tok >> 2) & (NG - 1))) * 16);
     };
-    const int vw0 = v_at(vr0), vw1 = v_at(vr1);
-    const int vs0 = St::VS + vr0 * NG + (D == 128 ? g >> 1 : g >> 2), vs1 = St::VS + vr1 * NG + (D == 128 ? g >> 1 : g >> 2);
+    const uint32_t va0 = v_at(lane >> 4), va1 = v_at((lane >> 4) + (D == 128 ? 2 : 0));
 
     for (; x < BR && pre[x] < hi; ++x) {
         const int p0 = pre[x], p1 = pre[x + 1];
@@ -280,29 +290,26 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
             __syncwarp();
         };
         constexpr int SP = St::SCALES / 16;
-        const int lane16 = lane * 16, vlane16 = D == 128 ? (lane ^ (((lane >> 3) & 1) << 1)) * 16 : lane16;
+        const int lane16 = lane * 16, vlane16 = (lane ^ ((lane >> 3) & (NG - 1))) * 16;
         auto issue = [&](int m, uint32_t dst) {
             if (m < nm) {
                 const int k = m & (kMeta - 1);
                 const ulonglong2 kv = meta.kv[k];
                 const unsigned long long sc = reinterpret_cast<const unsigned long long*>(&meta.sc[k])[(lane / SP) & 1];
-                // 16-byte pieces 0, 1 and 2, 3 of a value row change places in rows 2, 3, 6, 7, ...; the value
-                // scales follow the key scales in the stage; zeros where the page is not mapped
-                asm volatile("{\n\t.reg .pred p, q;\n\tsetp.lt.s32 p, %5, 256;\n\tsetp.ne.s32 q, %7, 0;\n\t"
-                             "cp.async.cg.shared.global [%0], [%2], 16, p;\n\t"
-                             "cp.async.cg.shared.global [%1 + %8], [%3], 16, p;\n\t"
-                             "@q cp.async.cg.shared.global [%0 + %6], [%4], 16, p;\n\t}\n" ::"r"(dst + lane16),
-                             "r"(dst + vlane16), "l"(kv.x + lane16), "l"(kv.y + lane16),
-                             "l"(sc + lane16 % (SP * 16)), "r"(meta.nv[k]), "n"(St::KS), "r"((int)(lane < 2 * SP)),
-                             "n"(St::V));
-                auto more = [&](auto off) {   // the pieces from 512 bytes on
-                    asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.s32 p, %4, 256;\n\t"
-                                 "cp.async.cg.shared.global [%0 + %5], [%2 + %5], 16, p;\n\t"
-                                 "cp.async.cg.shared.global [%1 + %6], [%3 + %5], 16, p;\n\t}\n" ::"r"(dst + lane16),
-                                 "r"(dst + vlane16), "l"(kv.x + lane16), "l"(kv.y + lane16), "r"(meta.nv[k]),
-                                 "n"(decltype(off)::value), "n"(St::V + decltype(off)::value));
-                };
-                each512<512, St::CODES>(more);
+                const int use = meta.nv[k];
+                const uint32_t kd = dst + lane16, vd = dst + vlane16;
+                const unsigned long long ka = kv.x + lane16, va = kv.y + lane16, sa = sc + lane16 % (SP * 16);
+                const int have = lane < 2 * SP;
+#define Q4_COPY(OFF) "cp.async.cg.shared.global [%0 + " #OFF "], [%2 + " #OFF "], 16, p;\n\t" \
+                     "cp.async.cg.shared.global [%1 + %8 + " #OFF "], [%3 + " #OFF "], 16, p;\n\t"
+#define Q4_COPIES(PIECES) asm volatile("{\n\t.reg .pred p, q;\n\tsetp.lt.s32 p, %5, 256;\n\tsetp.ne.s32 q, %7, 0;\n\t" \
+                     PIECES "@q cp.async.cg.shared.global [%0 + %6], [%4], 16, p;\n\t}\n" \
+                     ::"r"(kd), "r"(vd), "l"(ka), "l"(va), "l"(sa), "r"(use), "n"(St::KS), "r"(have), "n"(St::V))
+                if constexpr (St::CODES == 2048) Q4_COPIES(Q4_COPY(0) Q4_COPY(512) Q4_COPY(1024) Q4_COPY(1536));
+                else if constexpr (St::CODES == 1024) Q4_COPIES(Q4_COPY(0) Q4_COPY(512));
+                else Q4_COPIES(Q4_COPY(0));
+#undef Q4_COPIES
+#undef Q4_COPY
             }
             cp_async_commit();
         };
@@ -368,13 +375,19 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
             const float2 hf = __half22float2(h2(hi));
             qs[nt] = rest ? pack_f16(x0 - hf.x, x1 - hf.y) : D == 128 || t4 == 0 ? hi : 0u;
         }
-        float o[NT][MT][4], ref[NT][2], l[NT][2];
+        // o: tile 2 G + i holds rows of group G, elements 4 g + 2 i (rows g) and, 16 times as large, 4 g + 2 i + 1
+        // (rows g + 8); off: sums of P s for groups 2 k (rows g, all alike) and 2 k + 1 (rows g + 8)
+        float o[NT][MT][4], off[NT][NG / 2][4], ref[NT][2], l[NT][2];
+        float room = 9.f;                   // P is 2^room at the reference's logit ...
+        uint32_t above = 0x48484848u;       // ... + a scale byte: bit 7 where it is too large for that
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             ref[nt][0] = ref[nt][1] = -INFINITY;
             l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
             for (int m = 0; m < MT; ++m) o[nt][m][0] = o[nt][m][1] = o[nt][m][2] = o[nt][m][3] = 0.f;
+#pragma unroll
+            for (int k = 0; k < NG / 2; ++k) off[nt][k][0] = off[nt][k][1] = off[nt][k][2] = off[nt][k][3] = 0.f;
         }
 
         // The last granule of a pair may end before its last token: FULL = false.
@@ -387,6 +400,7 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
             __syncwarp();
             issue(m + kStages - 1, ring_a + nxt);
             const char* stg = ring + cur;
+            const uint32_t stg_a = ring_a + cur;
             nxt = cur;
             cur = cur == (kStages - 1) * St::BYTES ? 0 : cur + St::BYTES;
             const int nv = FULL ? kGran : meta.nv[m & (kMeta - 1)] & 255;
@@ -400,32 +414,34 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
                 const char* sc = stg + St::KS + u * 16 * NG;
                 uint32_t ka[NG], kb[NG], sa, sb;
                 if constexpr (D == 128) {
-                    const uint4 x4 = *reinterpret_cast<const uint4*>(ks + tk * 64 + t4 * 16);
-                    const uint4 y4 = *reinterpret_cast<const uint4*>(ks + (tk + 8) * 64 + t4 * 16);
+                    const uint4 x4 = *reinterpret_cast<const uint4*>(ks + g * 64 + t4 * 16);
+                    const uint4 y4 = *reinterpret_cast<const uint4*>(ks + (g + 8) * 64 + t4 * 16);
                     ka[0] = x4.x; ka[1] = x4.y; ka[2] = x4.z; ka[3] = x4.w;
                     kb[0] = y4.x; kb[1] = y4.y; kb[2] = y4.z; kb[3] = y4.w;
-                    sa = *reinterpret_cast<const uint32_t*>(sc + tk * 4);
-                    sb = *reinterpret_cast<const uint32_t*>(sc + (tk + 8) * 4);
+                    sa = *reinterpret_cast<const uint32_t*>(sc + g * 4);
+                    sb = *reinterpret_cast<const uint32_t*>(sc + (g + 8) * 4);
                 } else {
-                    const uint2 x2 = *reinterpret_cast<const uint2*>(ks + tk * 32 + t4 * 8);
-                    const uint2 y2 = *reinterpret_cast<const uint2*>(ks + (tk + 8) * 32 + t4 * 8);
+                    const uint2 x2 = *reinterpret_cast<const uint2*>(ks + g * 32 + t4 * 8);
+                    const uint2 y2 = *reinterpret_cast<const uint2*>(ks + (g + 8) * 32 + t4 * 8);
                     ka[0] = x2.x; ka[1] = x2.y;
                     kb[0] = y2.x; kb[1] = y2.y;
-                    sa = *reinterpret_cast<const uint16_t*>(sc + tk * 2);
-                    sb = *reinterpret_cast<const uint16_t*>(sc + (tk + 8) * 2);
+                    sa = *reinterpret_cast<const uint16_t*>(sc + g * 2);
+                    sb = *reinterpret_cast<const uint16_t*>(sc + (g + 8) * 2);
                 }
                 uint32_t fa[NG / 2], fb[NG / 2];   // scales of this lane's two tokens, f16x2
-#pragma unroll
-                for (int k = 0; k < NG / 2; ++k) {
-                    fa[k] = e4m3x2_to_f16x2(sa >> (16 * k));
-                    fb[k] = e4m3x2_to_f16x2(sb >> (16 * k));
+                if constexpr (D == 128) {
+                    e4m3x4_to_f16x4(sa, fa[0], fa[NG / 2 - 1]);
+                    e4m3x4_to_f16x4(sb, fb[0], fb[NG / 2 - 1]);
+                } else {
+                    fa[0] = e4m3x2_to_f16x2(sa);
+                    fb[0] = e4m3x2_to_f16x2(sb);
                 }
                 {
                     const uint32_t ua = (t4 & 1) ? fa[NG / 2 - 1] : fa[0], ub = (t4 & 1) ? fb[NG / 2 - 1] : fb[0];
                     const __half2 e8 = __float2half2_rn(0.00390625f);   // 2^-8: with the sums' 2^-13, 8 times 2^-24
-                    const uint32_t f[4] = {h2(__hmul2(h2(ua), e8)), h2(__hmul2(h2(ub), e8)), 0u, 0u};
+                    const uint32_t f[2] = {h2(__hmul2(h2(ua), e8)), h2(__hmul2(h2(ub), e8))};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f16_0(z[u][nt], f, qs[nt], 0u);
+                    for (int nt = 0; nt < NT; ++nt) mma_f16_k8(z[u][nt], f[0], f[1], qs[nt]);
                 }
 #pragma unroll
                 for (int gg = 0; gg < NG; ++gg) {
@@ -439,10 +455,8 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
                         float d[4];
                         mma_f16_0(d, f0, qf[nt][gg][0], qf[nt][gg][1]);
                         mma_f16(d, f1, qf[nt][gg][2], qf[nt][gg][3]);
-                        z[u][nt][0] = fmaf(xa, d[0], z[u][nt][0]);
-                        z[u][nt][1] = fmaf(xa, d[1], z[u][nt][1]);
-                        z[u][nt][2] = fmaf(xb, d[2], z[u][nt][2]);
-                        z[u][nt][3] = fmaf(xb, d[3], z[u][nt][3]);
+                        fma2(z[u][nt][0], z[u][nt][1], xa, d[0], d[1]);
+                        fma2(z[u][nt][2], z[u][nt][3], xb, d[2], d[3]);
                     }
                 }
             }
@@ -456,23 +470,37 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
 #pragma unroll
                     for (int e = 0; e < 4; ++e) tz[u][nt][e] = fmaf(z[u][nt][e], fac[nt][e & 1], e & 1 ? c1 : c0);
                     if (!FULL) {
-                        if (16 * u + tk >= nv) tz[u][nt][0] = tz[u][nt][1] = -INFINITY;
-                        if (16 * u + tk + 8 >= nv) tz[u][nt][2] = tz[u][nt][3] = -INFINITY;
+                        if (16 * u + g >= nv) tz[u][nt][0] = tz[u][nt][1] = -INFINITY;
+                        if (16 * u + g + 8 >= nv) tz[u][nt][2] = tz[u][nt][3] = -INFINITY;
                     }
                     most = fmaxf(most, fmaxf(fmaxf(tz[u][nt][0], tz[u][nt][1]), fmaxf(tz[u][nt][2], tz[u][nt][3])));
                 }
             }
-            if (__any_sync(0xffffffffu, most > 6.f)) {
+            // the value scales of the granule, a word per lane (some lanes alike)
+            constexpr int SW = St::SCALES / 4, TPW = 4 / NG;   // words, tokens per word
+            uint32_t sw = *reinterpret_cast<const uint32_t*>(stg + St::VS + lane % SW * 4);
+            if (!FULL) {
+                const int left = nv - lane % SW * TPW;
+                if (left < TPW) sw = left > 0 ? sw & 0xffffu : 0u;
+            }
+            if (__any_sync(0xffffffffu, most > room + 6.f || ((sw + above) & 0x80808080u))) {
+                uint32_t top = 0;   // the largest scale byte that is a number
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t byte = (sw >> (8 * k)) & 0x7fu;
+                    if (byte != 0x7fu) top = max(top, byte);
+                }
+                const float now = fminf(room, 15.f - (float)(__reduce_max_sync(0xffffffffu, top) >> 3));
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = ref[nt][e];
+                        float mx = ref[nt][e] + room;   // the largest logit that moved the reference so far
 #pragma unroll
                         for (int u = 0; u < U; ++u) {
                             float y0 = fmaf(z[u][nt][e], fac[nt][e], bias2), y1 = fmaf(z[u][nt][e + 2], fac[nt][e], bias2);
-                            if (!FULL && 16 * u + tk >= nv) y0 = -INFINITY;
-                            if (!FULL && 16 * u + tk + 8 >= nv) y1 = -INFINITY;
+                            if (!FULL && 16 * u + g >= nv) y0 = -INFINITY;
+                            if (!FULL && 16 * u + g + 8 >= nv) y1 = -INFINITY;
                             tz[u][nt][e] = y0;
                             tz[u][nt][e + 2] = y1;
                             mx = fmaxf(mx, fmaxf(y0, y1));
@@ -480,14 +508,18 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        const float base = mx == -INFINITY ? 0.f : mx, cr = exp2f(ref[nt][e] - base);
-                        ref[nt][e] = mx;
+                        const float base = mx == -INFINITY ? 0.f : mx - now, cr = exp2f(ref[nt][e] - base);
+                        ref[nt][e] = mx == -INFINITY ? mx : base;
                         l[nt][e] *= cr;
 #pragma unroll
                         for (int u = 0; u < U; ++u) { tz[u][nt][e] -= base; tz[u][nt][e + 2] -= base; }
 #pragma unroll
                         for (int k = 0; k < MT; ++k) { o[nt][k][e] *= cr; o[nt][k][e + 2] *= cr; }
+#pragma unroll
+                        for (int k = 0; k < NG / 2; ++k) { off[nt][k][e] *= cr; off[nt][k][e + 2] *= cr; }
                     }
+                room = now;
+                above = (uint32_t)(8.f * room) * 0x01010101u;
             }
             uint32_t pb[U][NT][2];
 #pragma unroll
@@ -504,47 +536,55 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
             // ---- O^T -----------------------------------------------------------------------------------
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                uint32_t vw[4][NW], sc[4];
+                // codes 4 g .. 4 g + 3 of each group, tokens 2 t4 and 2 t4 + 1 in the halves (b: + 8)
+                uint32_t a[NG], b[NG];
+                const uint32_t row = stg_a + u * 8 * D;
+                ldsm_x4_t(row + va0, a[0], b[0], a[1], b[1]);
+                if constexpr (D == 128) ldsm_x4_t(row + va1, a[2], b[2], a[3], b[3]);
+                uint32_t sl[NG], sh[NG];   // scales of these tokens, f16x2
+                {
+                    const char* sc = stg + St::VS + (16 * u + 2 * t4) * NG;
+                    uint32_t w[2][NG / 2];   // bytes (2 t4, G), (2 t4 + 1, G), (2 t4, G + 1), (2 t4 + 1, G + 1)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {   // rows vr0, vr1, vr0 + 8, vr1 + 8
-                    const int at = (k & 1 ? vw1 : vw0) + (16 * u + (k >> 1) * 8) * (D / 2);
-                    if constexpr (D == 128) {
-                        const uint2 x2 = *reinterpret_cast<const uint2*>(stg + at);
-                        vw[k][0] = x2.x; vw[k][1] = x2.y;
-                    } else {
-                        vw[k][0] = *reinterpret_cast<const uint32_t*>(stg + at);
-                    }
-                    sc[k] = *reinterpret_cast<const uint8_t*>(stg + (k & 1 ? vs1 : vs0) + (16 * u + (k >> 1) * 8) * NG);
-                    // beyond the query: whatever the page holds counts as 0
-                    if (!FULL && 16 * u + (k & 1 ? vr1 : vr0) + (k >> 1) * 8 >= nv) sc[k] = 0;
-                }
-                const uint32_t s01 = e4m3x2_to_f16x2(sc[0] | sc[1] << 8), s23 = e4m3x2_to_f16x2(sc[2] | sc[3] << 8);
-                // multipliers and offsets of the two code positions, for rows (vr0, vr1) and (+8)
-                const __half2 sx = __hmul2(h2(s01), __float2half2_rn(0.0625f)), sy = __hmul2(h2(s23), __float2half2_rn(0.0625f));
-                const __half2 lx = __hmul2(sx, __float2half2_rn(-1032.f)), ly = __hmul2(sy, __float2half2_rn(-1032.f));
-                const __half2 hx = __hmul2(sx, __float2half2_rn(-72.f)), hy = __hmul2(sy, __float2half2_rn(-72.f));
-                const __half2 tx = __hmul2(sx, __float2half2_rn(0.0625f)), ty = __hmul2(sy, __float2half2_rn(0.0625f));
-#pragma unroll
-                for (int w = 0; w < NW; ++w) {
-                    uint32_t xl = __byte_perm(vw[0][w], vw[1][w], 0x5410), xh = __byte_perm(vw[0][w], vw[1][w], 0x7632);
-                    uint32_t yl = __byte_perm(vw[2][w], vw[3][w], 0x5410), yh = __byte_perm(vw[2][w], vw[3][w], 0x7632);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t f[4];
-                        if (k & 1) {
-                            f[0] = h2(__hfma2(pick<0x00f000f0u>(xl, magic), tx, hx));
-                            f[1] = h2(__hfma2(pick<0x00f000f0u>(xh, magic), tx, hx));
-                            f[2] = h2(__hfma2(pick<0x00f000f0u>(yl, magic), ty, hy));
-                            f[3] = h2(__hfma2(pick<0x00f000f0u>(yh, magic), ty, hy));
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t x, y;
+                        if constexpr (D == 128) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(sc + 8 * k * NG);
+                            x = v.x;
+                            y = v.y;
                         } else {
-                            f[0] = h2(__hfma2(pick<0x000f000fu>(xl, magic), sx, lx));
-                            f[1] = h2(__hfma2(pick<0x000f000fu>(xh, magic), sx, lx));
-                            f[2] = h2(__hfma2(pick<0x000f000fu>(yl, magic), sy, ly));
-                            f[3] = h2(__hfma2(pick<0x000f000fu>(yh, magic), sy, ly));
+                            x = *reinterpret_cast<const uint32_t*>(sc + 8 * k * NG);
+                            y = x >> 16;
                         }
+                        if (!FULL) {   // beyond the query: whatever the page holds counts as 0
+                            if (16 * u + 2 * t4 + 8 * k >= nv) x = 0u;
+                            if (16 * u + 2 * t4 + 8 * k + 1 >= nv) y = 0u;
+                        }
+                        w[k][0] = __byte_perm(x, y, 0x5140);
+                        if constexpr (D == 128) w[k][1] = __byte_perm(x, y, 0x7362);
+                    }
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][w * 4 + k], f, pb[u][nt][0], pb[u][nt][1]);
-                        if (k == 1) { xl >>= 8; xh >>= 8; yl >>= 8; yh >>= 8; }
+                    for (int k = 0; k < NG / 2; ++k) {
+                        e4m3x4_to_f16x4(w[0][k], sl[2 * k], sl[2 * k + 1]);
+                        e4m3x4_to_f16x4(w[1][k], sh[2 * k], sh[2 * k + 1]);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < NG / 2; ++k) {
+                    const uint32_t f[4] = {sl[2 * k], sl[2 * k + 1], sh[2 * k], sh[2 * k + 1]};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(off[nt][k], f, pb[u][nt][0], pb[u][nt][1]);
+                }
+#pragma unroll
+                for (int gg = 0; gg < NG; ++gg) {
+                    const uint32_t a8 = __byte_perm(a[gg], 0u, 0x4341), b8 = __byte_perm(b[gg], 0u, 0x4341);
+                    const uint32_t f0[4] = {a[gg] & 0x000f000fu, a[gg] & 0x00ff00ffu, b[gg] & 0x000f000fu, b[gg] & 0x00ff00ffu};
+                    const uint32_t f1[4] = {a8 & 0x000f000fu, a8, b8 & 0x000f000fu, b8};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint32_t p0 = h2(__hmul2(h2(pb[u][nt][0]), h2(sl[gg]))), p1 = h2(__hmul2(h2(pb[u][nt][1]), h2(sh[gg])));
+                        mma_f16(o[nt][2 * gg], f0, p0, p1);
+                        mma_f16(o[nt][2 * gg + 1], f1, p0, p1);
                     }
                 }
             }
@@ -571,12 +611,14 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
                     mrg_l[warp][nt * 8 + 2 * t4 + e] = v;
                 }
 #pragma unroll
-                for (int w = 0; w < NW; ++w)
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh)
-                        *reinterpret_cast<float4*>(ob + (nt * 8 + 2 * t4 + e) * OLD + (g * NW + w) * 8 + hh * 4) =
-                            make_float4(o[nt][w * 4][e + 2 * hh], o[nt][w * 4 + 1][e + 2 * hh],
-                                        o[nt][w * 4 + 2][e + 2 * hh], o[nt][w * 4 + 3][e + 2 * hh]);
+                for (int gg = 0; gg < NG; ++gg) {
+                    // the codes' offset: 8 P s, in the accumulators' unit of 2^-24
+                    const float c8 = 4.76837158203125e-7f * off[nt][gg / 2][e + 2 * (gg & 1)];
+                    const float* a0 = o[nt][2 * gg];
+                    const float* a1 = o[nt][2 * gg + 1];
+                    *reinterpret_cast<float4*>(ob + (nt * 8 + 2 * t4 + e) * OLD + gg * kGrp + g * 4) = make_float4(
+                        a0[e] - c8, fmaf(a0[e + 2] - a0[e], 0.0625f, -c8), a1[e] - c8, fmaf(a1[e + 2] - a1[e], 0.0625f, -c8));
+                }
             }
         }
         __syncthreads();
@@ -688,7 +730,7 @@ __global__ void __launch_bounds__(D * kMergeY) q4_merge_kernel(Shape s, Attend a
                 sum = fmaf(ls[k], w, sum);
                 t = fmaf(acc[k][col], w, t);
             }
-            out[h * D + col] = __float2bfloat16_rn(n ? t * (16.f * exp2i(vexp)) / sum : 0.f);
+            out[h * D + col] = __float2bfloat16_rn(n ? t * exp2i(24 + vexp) / sum : 0.f);
         }
         __syncthreads();
     }

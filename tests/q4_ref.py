@@ -53,9 +53,10 @@ def summary(k, qbar):
     return w @ k / w.sum(), m, w.sum(), w @ k
 
 
-def attend(q, k, v, bias, k_scale):
+def attend(q, k, v, bias, k_scale, v_scale):
     """q [g, d], values k, v [n, d] of the cache, bias [n] (-inf: not attended).  Returns o [g, d] and the
-    bound of a kernel's error before the output's rounding: k_scale [n, d / 32] are the keys' scales (times 2^exp)."""
+    bound of a kernel's error before the output's rounding: k_scale, v_scale [n, d / 32] are the keys' and values'
+    scales (times 2^exp)."""
     d = q.shape[1]
     z = q @ k.T / np.sqrt(d) + bias
     zm = z.max(1, keepdims=True)
@@ -75,4 +76,14 @@ def attend(q, k, v, bias, k_scale):
     rel = 2.0 ** -11 + 2 * dz + 2.0 ** -20
     mass = p @ np.abs(v) / l
     err = rel[:, None] * (mass + np.abs(o)) + 2.0 ** -19 * np.abs(v[on]).sum(0) / l
+    # the weights times the values' scales, rounded to f16 (2^-12 relative), meet codes u of up to |u - 8| + 8, and 8
+    # times the unrounded sum comes off: 2^-12 p s u <= 2^-12 p (|v| + 8 s).  Below f16's normals the product is off
+    # by 2^-25, where the largest scale at weight 1 gives 1 or more (2^-9 * 2^9, or 2^(e - 7) * 2^(15 - e)): codes up
+    # to 15 make 15 * 2^-25 of that scale a token.  The sums of the products with u and with 8 run in fp32 and
+    # truncate by 2^-23 a step at most: two sums of up to 15 p s, in n / 16 steps shared by eight warps or more, and
+    # the merges: 2^-23 (n / 128 + 32) 30 p s
+    on_s = np.where(on[:, None], v_scale, 0.0)
+    heavy = np.repeat(p @ on_s / l, 32, axis=1)
+    err = err + 2.0 ** -12 * (mass + 8 * heavy) + 2.0 ** -21 * on.sum() * on_s.max() / l
+    err = err + 2.0 ** -23 * (on.sum() / 128 + 32) * 30 * heavy
     return o, err

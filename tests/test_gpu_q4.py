@@ -234,7 +234,7 @@ def _decode_ref(st, q, K, V, lens, hq, hkv, d, B, route, k_exp, v_exp):
                 for e in range(cnt):
                     bias[idx[e] * B:(idx[e] + 1) * B] = bs[e]
             bias[own * B:] = 0
-            o, e = R.attend(q[i, r * g:(r + 1) * g], kk[:, r], vv[:, r], bias, sk[:, r] * 2.0 ** k_exp)
+            o, e = R.attend(q[i, r * g:(r + 1) * g], kk[:, r], vv[:, r], bias, sk[:, r] * 2.0 ** k_exp, sv[:, r] * 2.0 ** v_exp)
             out[i, r * g:(r + 1) * g], err[i, r * g:(r + 1) * g] = o, e
     return out, err
 
@@ -313,8 +313,9 @@ def test_decode_long_equals_dequantised():
     for i, m in enumerate(lens):
         for r in range(hkv):
             k, v = K2[i, :m, r].double().cpu().numpy(), V2[i, :m, r].double().cpu().numpy()
-            s = np.abs(k).reshape(m, -1, 32).max(2) / 6.5   # an upper bound of the scales (max / scale >= 6.5)
-            ref, err = R.attend(q[i, r * 8:(r + 1) * 8].double().cpu().numpy(), k, v, np.zeros(m), s)
+            # upper bounds of the scales (max / scale >= 6.5)
+            ks, vs = (np.abs(x).reshape(m, -1, 32).max(2) / 6.5 for x in (k, v))
+            ref, err = R.attend(q[i, r * 8:(r + 1) * 8].double().cpu().numpy(), k, v, np.zeros(m), ks, vs)
             _check_out(o[i, r * 8:(r + 1) * 8], ref, err)
 
 
@@ -347,8 +348,8 @@ def test_unmapped_pages_count_as_zeros():
     o = st.decode(_q := _bf16(rng, b, hq, d).cuda())
     K2, V2 = (t[0, :, 0].double().cpu().numpy() for t in st.load(0, n))
     assert not K2[32:64].any() and not V2[96:128].any()
-    s = np.abs(K2).reshape(n, -1, 32).max(2) / 6.5
-    ref, err = R.attend(_q[0].double().cpu().numpy(), K2, V2, np.zeros(n), s)
+    ks, vs = (np.abs(x).reshape(n, -1, 32).max(2) / 6.5 for x in (K2, V2))
+    ref, err = R.attend(_q[0].double().cpu().numpy(), K2, V2, np.zeros(n), ks, vs)
     _check_out(o[0], ref, err)
 
 
@@ -362,6 +363,46 @@ def test_large_logits_and_moving_maximum():
     st.fill(K.cuda(), V.cuda(), [n])
     q = _bf16(rng, 1, hq, d, scale=2.0)
     ref, err = _decode_ref(st, q.double().numpy(), K.double().numpy(), V.double().numpy(), [n], hq, hkv, d, B, None, 4, 0)
+    _check_out(st.decode(q.cuda()), ref, err)
+
+
+@pytest.mark.parametrize("d,B,hq", [(128, 64, 8), (128, 16, 16), (64, 32, 4), (64, 16, 16)])
+def test_value_scales_of_all_sizes(d, B, hq):
+    """Values whose scales reach from the smallest to the largest, growing, falling or mixed along the sequence, each
+    output to within its bound; and a NaN among small values stays in its group."""
+    rng = np.random.default_rng(31)
+    n, b = 700, 4
+    st = _state(rng, b, 704, hq, 1, d, chunk=B, page=64, gamma=0.0)
+    size = np.exp2(np.linspace(-6.5, 11.5, n))
+    K, V = _bf16(rng, b, n, 1, d, scale=0.5), _bf16(rng, b, n, 1, d)
+    order = [np.arange(n), np.arange(n)[::-1], rng.permutation(n)]
+    for i in range(3):
+        V[i] = (V[i].float() * torch.from_numpy(size[order[i]]).float().view(n, 1, 1)).bfloat16()
+    V[3] = (V[3].float() * 2.0 ** -6).bfloat16()
+    st.fill(K.cuda(), V.cuda(), [n] * b)
+    q = _bf16(rng, b, hq, d)
+    ref, err = _decode_ref(st, q.double().numpy(), K.double().numpy(), V.double().numpy(), [n] * b, hq, 1, d, B, None, 0, 0)
+    _check_out(st.decode(q.cuda()), ref, err)
+    V[3, 100, 0, 40] = NAN
+    st.fill(K.cuda(), V.cuda(), [n] * b)
+    o = st.decode(q.cuda())
+    assert torch.isnan(o[3, :, 32:64]).all()
+    rest = [e for e in range(d) if not 32 <= e < 64]
+    _check_out(o[3:][..., rest], ref[3:][..., rest], err[3:][..., rest])
+
+
+def test_small_values_beside_a_strong_key():
+    """One key outweighs each of 3000 others by 2^16; their values are small, all of one sign, and still count."""
+    rng = np.random.default_rng(32)
+    n, hq, d, B = 3001, 4, 128, 64
+    st = _state(rng, 1, 3008, hq, 1, d, chunk=B, page=64, gamma=0.0)
+    K, V = torch.zeros(1, n, 1, d, dtype=torch.bfloat16), torch.full((1, n, 1, d), 2.0 ** -6, dtype=torch.bfloat16)
+    K[0, 5] = 1.0
+    V[0, 5] = 0.0
+    q = torch.full((1, hq, d), 11.0 / np.sqrt(d), dtype=torch.bfloat16)   # logit 11
+    st.fill(K.cuda(), V.cuda(), [n])
+    ref, err = _decode_ref(st, q.double().numpy(), K.double().numpy(), V.double().numpy(), [n], hq, 1, d, B, None, 0, 0)
+    assert err.max() < 0.3 * ref.min()   # the bound would notice if they were lost
     _check_out(st.decode(q.cuda()), ref, err)
 
 
