@@ -83,11 +83,11 @@ class Q4DecodeState:
         self.state = torch.zeros((batch, h_kv, d + 2), dtype=torch.float32, device=self.device)
         self.state[..., d] = -torch.inf
         self.seqlens = torch.zeros(batch, dtype=torch.int32, device=self.device)
-        self.qbar = qbar
         self.O = torch.empty((batch, h_q, d), dtype=torch.bfloat16, device=self.device)
         self._shape = dict(batch=batch, seqlen=capacity, h_q=h_q, h_kv=h_kv, d_h=d, chunk=chunk, alpha=alpha,
                            gamma=gamma, inv_sigma=inv_sigma, dtype=L.DASH_BF16)
         self.p = L.params(**self._shape)
+        self.qbar = qbar
         self._seen = {}   # arguments that passed the checks, by signature: their parameters
         self.kv = L.q4_kv(self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.page_table,
                           page_size=page_size, k_exp=k_exp, v_exp=v_exp)
@@ -95,6 +95,18 @@ class Q4DecodeState:
         self.workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=self.device)
         self._ws_bytes = self.workspace.shape[0]
         self.route = None
+
+    @property
+    def qbar(self):
+        """The learned query of Stage 0, float32 [h_kv, d] (checked when it is set)."""
+        return self._qbar
+
+    @qbar.setter
+    def qbar(self, q):
+        s = self._shape
+        if q is not None and not _need(q, "qbar", self.device, torch.float32, (s["h_kv"], s["d_h"])).is_contiguous():
+            raise ValueError("qbar must be contiguous")
+        self._qbar = q
 
     def _tokens(self, t, name):
         """t as [batch, n, h_kv, d] with contiguous d."""
@@ -108,6 +120,11 @@ class Q4DecodeState:
             raise ValueError(f"{name}: the head dimension must be contiguous")
         return t
 
+    def _rows(self, t, name):
+        """t: int32 [batch], contiguous (or None)."""
+        if t is not None and not _need(t, name, self.device, torch.int32, (self._shape["batch"],)).is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
     def _check(self, what, k, v, rows, name):
         """dash_params and token number for K/V arguments k, v and an int32 [batch] argument (or None)."""
         key = (what, _signature(k), _signature(v), _signature(rows))
@@ -117,12 +134,15 @@ class Q4DecodeState:
             k4, v4 = self._tokens(k, "K"), self._tokens(v, "V")
             if k4.shape[1] != v4.shape[1]:
                 raise ValueError("K and V hold different numbers of tokens")
-            if rows is not None and not _need(rows, name, self.device, torch.int32, (s["batch"],)).is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-            if len(self._seen) > 64:
-                self._seen.clear()
-            got = self._seen[key] = L.params(**s, k_strides=_st(k4), v_strides=_st(v4)), k4.shape[1]
+            self._rows(rows, name)
+            got = self._remember(key, (L.params(**s, k_strides=_st(k4), v_strides=_st(v4)), k4.shape[1]))
         return got
+
+    def _remember(self, key, value):
+        if len(self._seen) > 64:
+            self._seen.clear()
+        self._seen[key] = value
+        return value
 
     def append(self, k_new, v_new, counts=None, stream=None):
         """Append k_new, v_new [batch, n, h_kv, d] (or [batch, h_kv, d]: one token): the first
@@ -131,12 +151,9 @@ class Q4DecodeState:
             with _within(self.device, stream):
                 return self.append(k_new, v_new, counts)
         p, n = self._check("append", k_new, v_new, counts, "counts")
-        q = self.qbar
-        if _signature(q) != self._seen.get("qbar"):
-            s = self._shape
-            if not _need(q, "qbar", self.device, torch.float32, (s["h_kv"], s["d_h"])).is_contiguous():
-                raise ValueError("qbar must be contiguous")
-            self._seen["qbar"] = _signature(q)
+        q = self._qbar
+        if q is None:
+            raise TypeError("qbar is needed")
         rc = self._lib.dash_append_q4(p, self.kv, k_new.data_ptr(), v_new.data_ptr(), n,
                                       None if counts is None else counts.data_ptr(), q.data_ptr(), self.kbar.data_ptr(),
                                       self.state.data_ptr(), self.seqlens.data_ptr(), _current(self._index))
@@ -157,17 +174,31 @@ class Q4DecodeState:
         if _elsewhere(self._index, stream):
             with _within(self.device, stream):
                 return self.load(start, n, K, V)
-        if K is None:
-            s = self._shape
-            K = torch.empty((s["batch"], n, s["h_kv"], s["d_h"]), dtype=torch.bfloat16, device=self.device)
-        if V is None:
-            V = torch.empty_like(K, memory_format=torch.contiguous_format)
         rows = start if isinstance(start, torch.Tensor) else None
-        p, m = self._check("load", K, V, rows, "start")
-        if m != n:
-            raise ValueError(f"K and V must hold {n} tokens")
-        rc = self._lib.dash_load_q4(p, self.kv, None if rows is None else rows.data_ptr(), 0 if rows is not None else _int32(start, "start"), n,
-                                    self.seqlens.data_ptr(), K.data_ptr(), V.data_ptr(), _current(self._index))
+        if K is None and V is None:   # outputs of one's own need no checks
+            got = self._seen.get(n)
+            if got is None:
+                s = self._shape
+                like = self.O.new_empty(1).expand(s["batch"], n, s["h_kv"], s["d_h"])
+                strides = (n * s["h_kv"] * s["d_h"], s["h_kv"] * s["d_h"], s["d_h"])
+                got = self._remember(n, (like, L.params(**s, k_strides=strides, v_strides=strides)))
+            like, p = got
+            K = torch.empty_like(like, memory_format=torch.contiguous_format)
+            V = torch.empty_like(like, memory_format=torch.contiguous_format)
+            if _signature(rows) != self._seen.get("start"):
+                self._rows(rows, "start")
+                self._seen["start"] = _signature(rows)
+        else:
+            if K is None:
+                K = torch.empty_like(V, memory_format=torch.contiguous_format)
+            if V is None:
+                V = torch.empty_like(K, memory_format=torch.contiguous_format)
+            p, m = self._check("load", K, V, rows, "start")
+            if m != n:
+                raise ValueError(f"K and V must hold {n} tokens")
+        rc = self._lib.dash_load_q4(p, self.kv, None if rows is None else rows.data_ptr(),
+                                    0 if rows is not None else _int32(start, "start"), n, self.seqlens.data_ptr(),
+                                    K.data_ptr(), V.data_ptr(), _current(self._index))
         if rc:
             L._check(rc, "dash_load_q4")
         return K, V

@@ -596,6 +596,15 @@ def test_refusals():
         st.load(0, 3, k[:, :1].expand(-1, 3, -1, -1), k)      # all tokens in one place
     with pytest.raises(D.DashError):
         st.append(torch.zeros(2, 3, 2, 68, dtype=torch.bfloat16, device="cuda")[..., :64], k)   # rows 136 bytes apart
+    for bad in (st.qbar.double(), st.qbar.cpu(), st.qbar.T.contiguous().T, st.qbar[:1]):
+        with pytest.raises((TypeError, ValueError)):
+            st.qbar = bad
+    st.qbar = None
+    with pytest.raises(TypeError):
+        st.append(k, k)
+    st.load(0, 3, None, torch.empty(2, 3, 2, 64, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        st.load(0, 3, None, torch.empty(2, 4, 2, 64, dtype=torch.bfloat16, device="cuda"))
     big = D.Q4DecodeState(2, 64, 2, 1, 64, chunk=32, alpha=3.0, gamma=1.0, page_size=32)
     with pytest.raises(D.DashError):
         big.decode(big.O.clone())
