@@ -13,6 +13,7 @@
 //      registers: a Newton step is one pass over registers and one block barrier.  The heads' weights take the
 //      logits' place (in L2: reading them from the other blocks' shared memory took twice as long), and block
 //      k adds them up for the k-th quarter of the chunks.
+// Short rows take one block and one launch (route_short_kernel).
 // Measured with cold caches for 16 pairs of 2047 chunks and 16 heads of 128: logits 10.2 us (16.8 MB, 1.7 TB/s:
 // a read of this size is latency), the rest 14.7 (five Newton steps of about 1 us, two passes through L2, three
 // cluster barriers); one cluster for everything takes 25 to 26 us there, and 2 us more than these two
@@ -47,6 +48,31 @@ __device__ __forceinline__ int chunks_of(const Shape& s, const int* seqlens, int
     return max(0, min((seqlens[b] - 1) / s.B, s.T));
 }
 
+// The chunks' summaries of one 8-chunk tile: this lane's elements of chunk g8 (on: it is there).
+template <int D>
+__device__ __forceinline__ void load_tile(float2 (&u)[D / 16][2], const float* p, bool on)
+{
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        u[kk][0] = on ? __ldg(reinterpret_cast<const float2*>(p + kk * 16)) : make_float2(0.f, 0.f);
+        u[kk][1] = on ? __ldg(reinterpret_cast<const float2*>(p + kk * 16 + 8)) : make_float2(0.f, 0.f);
+    }
+}
+// acc += q u^T: heads g8 and g8 + 8, chunks 2 t4 and 2 t4 + 1
+template <int D>
+__device__ __forceinline__ void tile_logits(float* acc, const uint32_t (&qf)[D / 16][4], const float2 (&u)[D / 16][2])
+{
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t h0, m0, l0, h1, m1, l1;
+        split3(u[kk][0], h0, m0, l0);
+        split3(u[kk][1], h1, m1, l1);
+        mma_bf16(acc, qf[kk], l0, l1);
+        mma_bf16(acc, qf[kk], m0, m1);
+        mma_bf16(acc, qf[kk], h0, h1);
+    }
+}
+
 // X [pair][head][T]: the logits of the complete chunks before each query's own.
 template <int D>
 __global__ void __launch_bounds__(32 * kLogitWarps) route_logits_kernel(Shape s, const __nv_bfloat16* __restrict__ q,
@@ -65,14 +91,7 @@ __global__ void __launch_bounds__(32 * kLogitWarps) route_logits_kernel(Shape s,
     const float* kb = kbar + ((long long)br * s.T + c0 + g8) * D + 2 * t4;
     float2 u[kTiles][D / 16][2];
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            const bool on = c0 + t * 8 + g8 < nv;
-            const float* p = kb + t * 8 * D + kk * 16;
-            u[t][kk][0] = on ? __ldg(reinterpret_cast<const float2*>(p)) : make_float2(0.f, 0.f);
-            u[t][kk][1] = on ? __ldg(reinterpret_cast<const float2*>(p + 8)) : make_float2(0.f, 0.f);
-        }
+    for (int t = 0; t < kTiles; ++t) load_tile<D>(u[t], kb + t * 8 * D, c0 + t * 8 + g8 < nv);
     uint32_t qf[D / 16][4];
     const __nv_bfloat16* qb = q + ((long long)b * s.hq + r * G) * D;
     load_q_frags<D>(qf, [&](int h) -> const __nv_bfloat16* { return h < G ? qb + (long long)h * D : nullptr; });
@@ -81,15 +100,7 @@ __global__ void __launch_bounds__(32 * kLogitWarps) route_logits_kernel(Shape s,
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t h0, m0, l0, h1, m1, l1;
-            split3(u[t][kk][0], h0, m0, l0);
-            split3(u[t][kk][1], h1, m1, l1);
-            mma_bf16(acc, qf[kk], l0, l1);
-            mma_bf16(acc, qf[kk], m0, m1);
-            mma_bf16(acc, qf[kk], h0, h1);
-        }
+        tile_logits<D>(acc, qf, u[t]);
         const int c = c0 + t * 8 + 2 * t4;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -320,6 +331,122 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThr, 1)
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // no block leaves while its memory is read
 }
 
+// Short rows (at most 32 V chunks): one block per pair does all of it.  The tiles are shared by the warps, the
+// logits stay in shared memory, and a head is one warp's, whose Newton steps need no barrier.
+template <int D, int V>
+__global__ void __launch_bounds__(512) route_short_kernel(Shape s, const __nv_bfloat16* __restrict__ q,
+                                                          const float* __restrict__ kbar, const int* __restrict__ seqlens,
+                                                          Routes rt, int* status)
+{
+    constexpr int LD = 32 * V + 4;   // floats per head
+    __shared__ float x[16][LD], lsum[V];
+    __shared__ int csum[V];
+    pdl_wait();   // the append of this step
+    pdl_launch_dependents();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
+    const int br = blockIdx.x, b = br / s.hkv, r = br % s.hkv, G = s.g, warps = blockDim.x >> 5;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
+    const int nv = chunks_of(s, seqlens, b);
+    if (warp * 8 < nv) {
+        uint32_t qf[D / 16][4];
+        const __nv_bfloat16* qb = q + ((long long)b * s.hq + r * G) * D;
+        load_q_frags<D>(qf, [&](int h) -> const __nv_bfloat16* { return h < G ? qb + (long long)h * D : nullptr; });
+        const float scale = (s.alpha - 1.f) * s.gamma * rsqrtf((float)D);
+        for (int c0 = warp * 8; c0 < nv; c0 += warps * 8) {
+            float2 u[D / 16][2];
+            load_tile<D>(u, kbar + ((long long)br * s.T + c0 + g8) * D + 2 * t4, c0 + g8 < nv);
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            tile_logits<D>(acc, qf, u);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[g8 + (e >> 1) * 8][c0 + 2 * t4 + (e & 1)] = acc[e] * scale;
+        }
+    }
+    __syncthreads();
+
+    // ---- threshold of head `warp`; its weights take the logits' place --------------------------------
+    const float p = 1.f / (s.alpha - 1.f);
+    const int mode = ent_mode(s.alpha);
+    if (warp < G && nv > 0) {
+        float v[V], mx = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            v[k] = lane + 32 * k < nv ? x[warp][lane + 32 * k] : -INFINITY;
+            mx = fmaxf(mx, v[k]);
+        }
+        mx = warp_max(mx);
+        float lo = mx - 1.f, t = lo, hi = mx - exp2f(-(s.alpha - 1.f) * __log2f((float)nv));
+        for (int it = 0; it < kMaxIter; ++it) {
+            float f = 0.f, fd = 0.f;
+            sums<V>(v, t, p, mode, f, fd);
+            f = warp_sum(f);
+            fd = warp_sum(fd);
+            if (newton(f, fd, t, lo, hi, s.alpha, mode)) break;
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const float u = fmaxf(v[k] - t, 0.f);
+            x[warp][lane + 32 * k] = mode == 2 ? u * u : mode == 1 ? u : power(u, p);
+        }
+    }
+    __syncthreads();
+
+    // ---- group weights, a warp per 32 chunks; ascending lists -----------------------------------------
+    float w = 0.f, lw = 0.f;
+    uint32_t m = 0;
+    if (warp < V && warp * 32 < nv) {
+        if (tid < nv) {
+            for (int k = 0; k < G; ++k) w += x[k][tid];
+            w *= 1.f / G;
+        }
+        m = __ballot_sync(0xffffffffu, w > 0.f);
+        lw = w > 0.f ? __logf(w) : 0.f;
+        const float sl = warp_sum(lw);
+        if (lane == 0) { lsum[warp] = sl; csum[warp] = __popc(m); }
+    } else if (warp < V && lane == 0) {
+        lsum[warp] = 0.f;
+        csum[warp] = 0;
+    }
+    __syncthreads();
+    float all = 0.f;
+    int total = 0, at = 0;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        all += lsum[k];
+        at += k < warp ? csum[k] : 0;
+        total += csum[k];
+    }
+    if (m >> lane & 1) {
+        const long long j = (long long)br * rt.cap + at + __popc(m & ((1u << lane) - 1u));
+        rt.idx[j] = tid;
+        rt.bias[j] = (lw - all / total) * s.inv_sigma;
+    }
+    if (tid == 0) rt.counts[br] = total;
+    if (rt.bitmask && lane == 0 && warp < rt.words) rt.bitmask[(long long)br * rt.words + warp] = warp < V ? m : 0u;
+}
+
+// Where one block does it all.  Up to 512 chunks (16 entries per lane), and as long as reading the summaries with
+// one SM costs less than the launch and the cluster barriers that it saves: d = 64, 24 chunks 16.4 -> 12.3 us
+// a call, 500 chunks 21.2 -> 17.6; d = 128, 127 chunks 25.4 -> 22.3, 255 chunks 26.7 -> 25.1, 300 chunks 21.1 ->
+// 19.7, but 511 chunks 29.7 -> 30.5.
+bool short_row(const Shape& s) { return s.T <= 512 && s.T * s.d <= 40960; }
+
+template <int D, int V>
+cudaError_t short_t(const Shape& s, const void* q, const float* kbar, const int* seqlens, const Routes& rt, int* status,
+                    cudaStream_t st)
+{
+    // a warp per head, per 32 chunks, and (up to 16) per tile
+    int warps = s.g > V ? s.g : V;
+    while (warps < 16 && warps * 8 < s.T) warps *= 2;
+    return launch_after(route_short_kernel<D, V>, dim3(s.batch * s.hkv), dim3(32 * warps), 0, st, s,
+                        (const __nv_bfloat16*)q, kbar, seqlens, rt, status);
+}
+template <int V>
+cudaError_t short_v(const Shape& s, const void* q, const float* kbar, const int* seqlens, const Routes& rt, int* status,
+                    cudaStream_t st)
+{
+    return s.d == 128 ? short_t<128, V>(s, q, kbar, seqlens, rt, status, st) : short_t<64, V>(s, q, kbar, seqlens, rt, status, st);
+}
+
 template <int V>
 cudaError_t solve_t(const Shape& s, float* X, const int* seqlens, const Routes& rt, int* status, cudaStream_t st)
 {
@@ -335,6 +462,9 @@ bool route_q4_supported(const Shape& s) { return s.T > 0 && vals_per_thread(s) <
 cudaError_t launch_route_q4(const Shape& s, const void* q, const float* kbar, const int* seqlens, const Routes& rt,
                             float* X, int* status, cudaStream_t st)
 {
+    if (short_row(s))
+        return s.T <= 128 ? short_v<4>(s, q, kbar, seqlens, rt, status, st)
+                          : s.T <= 256 ? short_v<8>(s, q, kbar, seqlens, rt, status, st) : short_v<16>(s, q, kbar, seqlens, rt, status, st);
     const long long units = (long long)s.batch * s.hkv * ((s.T + 8 * kTiles - 1) / (8 * kTiles));
     const dim3 grid((unsigned)((units + kLogitWarps - 1) / kLogitWarps));
     const cudaError_t e = launch_after(s.d == 128 ? route_logits_kernel<128> : route_logits_kernel<64>, grid,

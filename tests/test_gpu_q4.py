@@ -646,6 +646,14 @@ def test_load_and_append_nothing():
     (16, 1, 64, 16, 57600, [57000, 40], 2.0, 5.0, 1.0),            # 32 entries per thread
     (8, 1, 64, 16, 40000, [39990], 1.8, 2.0, 1.0),
     (1, 1, 64, 16, 320000, [310000], 1.5, 8.0, 1.0),               # more than the cluster's registers hold
+    # one block per row: up to 128, 256 and 512 chunks, the last places and the first beyond
+    (4, 2, 64, 32, 1000, [999, 33, 32, 1], 1.5, 3.0, 1.0),
+    (16, 1, 128, 16, 2048, [2048, 2033, 16], 1.25, 4.0, 0.5),
+    (1, 3, 128, 128, 32767, [32767, 16640], 2.0, 5.0, 1.0),
+    (2, 2, 128, 64, 20480, [20480, 20417, 1], 1.5, 6.0, 1.0),
+    (8, 1, 128, 64, 20544, [20544], 1.5, 6.0, 1.0),
+    (16, 2, 64, 16, 8192, [8192, 4100], 1.5, 6.0, 1.0),
+    (8, 2, 64, 16, 8208, [8208, 8191], 2.0, 6.0, 1.0),
 ])
 def test_routes_against_the_oracle(g, hkv, d, B, cap, lens, alpha, gamma, inv_sigma):
     """Routed sets by the margin rule, biases within what the logits' error does to log w, bitmask, for every way the
