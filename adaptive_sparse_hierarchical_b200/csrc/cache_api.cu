@@ -199,8 +199,9 @@ int dash_decode_q4(const dash_params* p, const dash_q4_kv* kv, const void* q, co
     const Shape s = shape_of(p);
     // the pairs' granules (16 tokens or more) are numbered in 32 bits
     if ((long long)p->batch * p->h_kv * (p->seqlen / 16 + 1ll) > 0x7fffffffll) return DASH_EUNSUPPORTED;
-    // Stage 1 keeps every head's logits of one (sequence, KV head) in shared memory
-    if (routed && (size_t)s.g * (size_t)s.T * 4 > 225 * 1024) return DASH_EUNSUPPORTED;
+    // where the routing of q4_route.cu stops, Stage 1 keeps every head's logits of one (sequence, KV head) in shared
+    // memory
+    if (routed && !route_q4_supported(s) && (size_t)s.g * (size_t)s.T * 4 > 225 * 1024) return DASH_EUNSUPPORTED;
     const Q4Layout L = q4_layout(p);
     if (!workspace || ws_bytes < L.total) return DASH_EWORKSPACE;
     if (!on(workspace, kAlign)) return DASH_EALIGN;

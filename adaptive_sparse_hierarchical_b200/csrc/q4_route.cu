@@ -1,5 +1,5 @@
 // q4_route.cu -- Stage 1 of decoding for the 4-bit cache's decode: chunk logits over the whole GPU, then
-// thresholds and route lists with the heads of a group spread over a cluster.
+// thresholds of the heads and the pairs' route lists.
 //
 // The quantities are those of stage1_decode.cu (Eq. 6 and Proposition 4.1):
 //   x_c^(h) = (alpha-1) gamma <q^(h), kbar_c>/sqrt(d),  what = [x - tau]_+^{1/(alpha-1)},  w = mean over heads,
@@ -9,15 +9,16 @@
 // and has every head's threshold solved on a list that crosses blocks.  Here
 //   1. a warp takes 16 chunks of a pair, reads their summaries once (all loads in flight together) and
 //      writes the group's logits: HBM-bound, 4 d bytes per chunk;
-//   2. in a cluster of 4 blocks per pair each block owns a quarter of the heads and keeps their whole rows in
-//      registers: a Newton step is one pass over registers and one block barrier.  The heads' weights take the
-//      logits' place (in L2: reading them from the other blocks' shared memory took twice as long), and block
-//      k adds them up for the k-th quarter of the chunks.
-// Short rows take one block and one launch (route_short_kernel).
-// Measured with cold caches for 16 pairs of 2047 chunks and 16 heads of 128: logits 10.2 us (16.8 MB, 1.7 TB/s:
-// a read of this size is latency), the rest 14.7 (five Newton steps of about 1 us, two passes through L2, three
-// cluster barriers); one cluster for everything takes 25 to 26 us there, and 2 us more than these two
-// together when a step follows another (a whole routed call 66 -> 62 us).  Clusters of 8 are slower: 15 of 16 fit.
+//   2. a block per (pair, head) holds the head's row in registers: a Newton step is one pass over them and one
+//      block barrier.  The weights take the logits' place (in L2);
+//   3. in a cluster of 4 blocks per pair each block adds up the heads' weights for a quarter of the chunks, and
+//      the blocks tell each other their counts and sums of logarithms.
+// Short rows take one block and one launch instead (route_short_kernel).
+// Measured: with cold caches 16 pairs of 2047 chunks and 16 heads of 128 take 10 us for the logits (16.8 MB, 1.7
+// TB/s: a read of this size is latency); one cluster for everything takes 25 to 26 us there.  Whole calls: steps 2
+// and 3 in one kernel, with the heads spread over the cluster's blocks, are 1 us slower there (36.3 against
+// 35.3) and 15 us with 128 pairs (79.6 against 64.1): a launch costs less than a cluster barrier, and blocks of
+// one head fill the GPU.  Clusters of 8 are slower: 15 of 16 fit.
 #include <cooperative_groups.h>
 
 #include "entmax.cuh"
@@ -115,21 +116,12 @@ struct Cross {     // what a block tells the others of its cluster about its qua
     int cnt;
 };
 
-// heads_per_block heads share the block's 16 warps; a head takes as few of its warps (a power of two) as
-// keep 8 entries or less per thread: the fewer, the less there is to add up in a step, and a head in a
-// single warp needs no barrier at all.
-__host__ __device__ inline int heads_per_block(int g) { return (g + kCl - 1) / kCl; }
-__host__ __device__ inline int warps_per_head(int g, int T)
+// Warps of a head: as few (a power of two) as leave 16 entries or less per thread.
+inline int warps_per_head(int T)
 {
-    const int most = kWarps / heads_per_block(g);   // g is a power of two: so is this
     int w = 1;
-    while (w < most && T > 8 * 32 * w) w *= 2;
+    while (w < kWarps && T > 16 * 32 * w) w *= 2;
     return w;
-}
-inline int vals_per_thread(const Shape& s)
-{
-    const int lanes = 32 * warps_per_head(s.g, s.T);
-    return (s.T + lanes - 1) / lanes;
 }
 
 // Chunks per block in the last phase: whole 32-chunk words.
@@ -187,77 +179,76 @@ __device__ __forceinline__ bool newton(float f, float fd, float& t, float& lo, f
     return false;
 }
 
+// Thresholds: a block per (pair, head).  The head's weights [x - tau]_+^p take its logits' place in X.
 template <int V>
+__global__ void __launch_bounds__(kThr) route_tau_kernel(Shape s, float* X, const int* __restrict__ seqlens, int* status)
+{
+    __shared__ float red[kWarps];
+    __shared__ float2 part[2][kWarps];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, step = blockDim.x, warps = step >> 5;
+    if (blockIdx.x == 0 && tid == 0) *status = 0;
+    const int nv = chunks_of(s, seqlens, blockIdx.x / (s.g * s.hkv));
+    if (nv == 0) return;
+    const float p = 1.f / (s.alpha - 1.f);
+    const int mode = ent_mode(s.alpha);
+    float v[V], mx = -INFINITY;
+    float* row = X + (long long)blockIdx.x * s.T;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        v[k] = tid + k * step < nv ? row[tid + k * step] : -INFINITY;
+        mx = fmaxf(mx, v[k]);
+    }
+    mx = warp_max(mx);
+    if (warps > 1) {
+        if (lane == 0) red[warp] = mx;
+        __syncthreads();
+        for (int k = 0; k < warps; ++k) mx = fmaxf(mx, red[k]);
+    }
+    // Newton steps from max - 1, at most one barrier each
+    float lo = mx - 1.f, t = lo, hi = mx - exp2f(-(s.alpha - 1.f) * __log2f((float)nv));
+    for (int it = 0; it < kMaxIter; ++it) {
+        float f = 0.f, fd = 0.f;
+        sums<V>(v, t, p, mode, f, fd);
+        f = warp_sum(f);
+        fd = warp_sum(fd);
+        if (warps > 1) {
+            if (lane == 0) part[it & 1][warp] = make_float2(f, fd);
+            __syncthreads();   // a buffer is written again two steps, and a barrier, later
+            f = fd = 0.f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                if (k >= warps) break;
+                const float2 o = part[it & 1][k];
+                f += o.x;
+                fd += o.y;
+            }
+        }
+        if (newton(f, fd, t, lo, hi, s.alpha, mode)) break;   // the same numbers in every thread
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+        if (tid + k * step < nv) {
+            const float u = fmaxf(v[k] - t, 0.f);
+            __stcg(row + tid + k * step, mode == 2 ? u * u : mode == 1 ? u : power(u, p));
+        }
+}
+
+// Group weights and lists: a cluster of 4 blocks per pair, a quarter of the chunks each.
 __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThr, 1)
-    route_solve_kernel(Shape s, float* X, const int* __restrict__ seqlens, Routes rt, int* status)
+    route_list_kernel(Shape s, const float* X, const int* __restrict__ seqlens, Routes rt)
 {
     extern __shared__ float keep[];   // the weights of this block's quarter of the chunks
-    __shared__ float red[kWarps], lsum[kWarps];
-    __shared__ float2 part[2][kWarps];
+    __shared__ float lsum[kWarps];
     __shared__ int csum[kWarps];
     __shared__ Cross cx;
     cg::cluster_group cl = cg::this_cluster();
     pdl_wait();
     pdl_launch_dependents();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
-    const int rank = (int)cl.block_rank(), br = blockIdx.x / kCl, b = br / s.hkv, G = s.g;
+    const int rank = (int)cl.block_rank(), br = blockIdx.x / kCl, G = s.g;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int nv = chunks_of(s, seqlens, b);
-    const int hb = heads_per_block(G), wph = warps_per_head(G, s.T);
-    const int hl = warp / wph, h = rank * hb + hl, sub = (warp & (wph - 1)) * 32 + lane, step = wph * 32;
-    const bool mine = hl < hb && h < G, active = mine && nv > 0;
-    const float p = 1.f / (s.alpha - 1.f);
-    const int mode = ent_mode(s.alpha);
-
-    // ---- this thread's logits of head h; the head's maximum --------------------------------------
-    float v[V], mx = -INFINITY;
-    float* row = X + ((long long)br * G + h) * s.T;
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        v[k] = active && sub + k * step < nv ? row[sub + k * step] : -INFINITY;
-        mx = fmaxf(mx, v[k]);
-    }
-    mx = warp_max(mx);
-    if (wph > 1) {
-        if (lane == 0) red[warp] = mx;
-        __syncthreads();
-        for (int k = 0; k < wph; ++k) mx = fmaxf(mx, red[(hl * wph + k) & (kWarps - 1)]);
-    }
-
-    // ---- threshold: Newton steps from max - 1, at most one barrier each ---------------------------
-    float lo = mx - 1.f, t = lo, hi = active ? mx - exp2f(-(s.alpha - 1.f) * __log2f((float)nv)) : 0.f;
-    bool done = !active;
-    for (int it = 0; it < kMaxIter; ++it) {
-        float f = 0.f, fd = 0.f;
-        if (!done) {
-            sums<V>(v, t, p, mode, f, fd);
-            f = warp_sum(f);
-            fd = warp_sum(fd);
-        }
-        if (wph > 1) {
-            if (lane == 0 && !done) part[it & 1][warp] = make_float2(f, fd);
-            if (__syncthreads_and(done)) break;   // a buffer is written again two steps, and a barrier, later
-            f = fd = 0.f;
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                if (k >= wph) break;
-                const float2 o = part[it & 1][(hl * wph + k) & (kWarps - 1)];
-                f += o.x;
-                fd += o.y;
-            }
-        } else if (done) {
-            break;
-        }
-        if (!done) done = newton(f, fd, t, lo, hi, s.alpha, mode);
-    }
-    if (mine)
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-            if (sub + k * step < nv) {
-                const float u = fmaxf(v[k] - t, 0.f);
-                __stcg(row + sub + k * step, mode == 2 ? u * u : mode == 1 ? u : power(u, p));   // over the logit
-            }
-    cl.sync();
+    const int nv = chunks_of(s, seqlens, br / s.hkv);
 
     // ---- group weights of this block's quarter of the chunks, in whole 32-chunk words --------------
     const int per = quarter(nv), c_lo = min(nv, rank * per), c_hi = min(nv, c_lo + per);
@@ -448,16 +439,16 @@ cudaError_t short_v(const Shape& s, const void* q, const float* kbar, const int*
 }
 
 template <int V>
-cudaError_t solve_t(const Shape& s, float* X, const int* seqlens, const Routes& rt, int* status, cudaStream_t st)
+cudaError_t tau_t(const Shape& s, float* X, const int* seqlens, int* status, cudaStream_t st)
 {
-    return launch_after(route_solve_kernel<V>, dim3(kCl * s.batch * s.hkv), dim3(kThr), quarter(s.T) * 4, st, s, X,
-                        seqlens, rt, status);
+    return launch_after(route_tau_kernel<V>, dim3(s.batch * s.hkv * s.g), dim3(32 * warps_per_head(s.T)), 0, st, s, X, seqlens,
+                        status);
 }
 
 }  // namespace
 
-// A thread holds at most 32 entries, a block the weights of a quarter of the chunks (static shared memory aside).
-bool route_q4_supported(const Shape& s) { return s.T > 0 && vals_per_thread(s) <= kMaxVals && quarter(s.T) * 4 <= 46 * 1024; }
+// A thread holds at most 32 entries (a quarter of the chunks' weights is then less than a block's shared memory).
+bool route_q4_supported(const Shape& s) { return s.T > 0 && s.T <= kMaxVals * kThr; }
 
 cudaError_t launch_route_q4(const Shape& s, const void* q, const float* kbar, const int* seqlens, const Routes& rt,
                             float* X, int* status, cudaStream_t st)
@@ -467,12 +458,13 @@ cudaError_t launch_route_q4(const Shape& s, const void* q, const float* kbar, co
                           : s.T <= 256 ? short_v<8>(s, q, kbar, seqlens, rt, status, st) : short_v<16>(s, q, kbar, seqlens, rt, status, st);
     const long long units = (long long)s.batch * s.hkv * ((s.T + 8 * kTiles - 1) / (8 * kTiles));
     const dim3 grid((unsigned)((units + kLogitWarps - 1) / kLogitWarps));
-    const cudaError_t e = launch_after(s.d == 128 ? route_logits_kernel<128> : route_logits_kernel<64>, grid,
+    cudaError_t e = launch_after(s.d == 128 ? route_logits_kernel<128> : route_logits_kernel<64>, grid,
                                        dim3(32 * kLogitWarps), 0, st, s, (const __nv_bfloat16*)q, kbar, seqlens, X);
     if (e != cudaSuccess) return e;
-    const int v = vals_per_thread(s);
-    return v <= 4 ? solve_t<4>(s, X, seqlens, rt, status, st)
-                  : v <= 16 ? solve_t<16>(s, X, seqlens, rt, status, st) : solve_t<kMaxVals>(s, X, seqlens, rt, status, st);
+    e = s.T <= 16 * kThr ? tau_t<16>(s, X, seqlens, status, st) : tau_t<kMaxVals>(s, X, seqlens, status, st);
+    if (e != cudaSuccess) return e;
+    return launch_after(route_list_kernel, dim3(kCl * s.batch * s.hkv), dim3(kThr), quarter(s.T) * 4, st, s, (const float*)X,
+                        seqlens, rt);
 }
 
 }  // namespace dash

@@ -93,11 +93,13 @@ def test_bad_calls():
     assert dec(w=None) == L.DASH_EWORKSPACE and dec(n=ws - 1) == L.DASH_EWORKSPACE
     assert dec(w=384) == L.DASH_EALIGN and dec(q=264) == L.DASH_EALIGN
     assert dec(p=_p(batch=2000), n=1 << 50) == L.DASH_EUNSUPPORTED       # 4000 pairs
-    # routing 16 heads of 4096 chunks does not fit its shared memory; dense decoding needs no routing, so only the
-    # workspace is missed here
-    big = dict(h_q=32, seqlen=131072, chunk=32)
-    assert dec(p=_p(**big), kv=_kv(max_pages=1024), n=1 << 50) == L.DASH_EUNSUPPORTED
-    assert dec(p=_p(**big, gamma=0.0), kv=_kv(max_pages=1024), kb=None, n=16) == L.DASH_EWORKSPACE
+    # routing 16 heads of 32768 chunks fits neither way of doing it; dense decoding needs no routing, so only the
+    # workspace is missed here, as with 16384 chunks
+    big = dict(h_q=32, seqlen=524288, chunk=16)
+    assert dec(p=_p(**big), kv=_kv(max_pages=4096), n=1 << 50) == L.DASH_EUNSUPPORTED
+    assert dec(p=_p(**big, gamma=0.0), kv=_kv(max_pages=4096), kb=None, n=16) == L.DASH_EWORKSPACE
+    big["seqlen"] = 262144
+    assert dec(p=_p(**big), kv=_kv(max_pages=4096), n=16) == L.DASH_EWORKSPACE
     assert dec(p=_p(gamma=0.0), kb=None, r=L.route_out(256), n=1 << 50) == L.DASH_EINVAL   # routes asked for
     # more granules than 32 bits number: 2048 pairs of 2^25 tokens
     huge = _p(batch=1024, seqlen=1 << 25, chunk=128, gamma=0.0)

@@ -611,17 +611,17 @@ def test_refusals():
 
 
 def test_dense_needs_no_room_for_routing():
-    """Chunk logits of 16 heads x 4096 chunks do not fit the routing's shared memory; dense decoding has none."""
+    """16 heads x 32768 chunks are more than the routing takes; dense decoding has none."""
     rng = np.random.default_rng(25)
-    hq, hkv, d, B, page, n = 16, 1, 64, 32, 64, 500
+    hq, hkv, d, B, page, n = 16, 1, 64, 16, 64, 500
     kw = dict(chunk=B, page=page)
-    st = _state(rng, 1, 131072, hq, hkv, d, gamma=0.0, **kw)
+    st = _state(rng, 1, 524288, hq, hkv, d, gamma=0.0, **kw)
     K, V = _bf16(rng, 1, n, hkv, d), _bf16(rng, 1, n, hkv, d)
     st.fill(K.cuda(), V.cuda(), [n])
     q = _bf16(rng, 1, hq, d)
     ref, err = _decode_ref(st, q.double().numpy(), K.double().numpy(), V.double().numpy(), [n], hq, hkv, d, B, None, 0, 0)
     _check_out(st.decode(q.cuda()), ref, err)
-    st = _state(rng, 1, 131072, hq, hkv, d, gamma=1.0, **kw)
+    st = _state(rng, 1, 524288, hq, hkv, d, gamma=1.0, **kw)
     with pytest.raises(D.DashError):
         st.decode(q.cuda())
 
@@ -638,14 +638,15 @@ def test_load_and_append_nothing():
 
 
 @pytest.mark.parametrize("g,hkv,d,B,cap,lens,alpha,gamma,inv_sigma", [
-    (8, 2, 128, 64, 2048, [2000, 65, 64], 1.5, 6.0, 1.0),          # a warp per head, few entries
+    (8, 2, 128, 64, 2048, [2000, 65, 64], 1.5, 6.0, 1.0),          # 4 warps per head
     (4, 2, 128, 32, 8192, [8000, 1], 2.0, 4.0, 0.5),
     (2, 1, 64, 16, 4096, [4095, 17, 4081], 1.25, 3.0, 1.0),
-    (1, 2, 64, 16, 16384, [16000, 9000], 1.5, 8.0, 0.0),           # 4 warps per head
+    (1, 2, 64, 16, 16384, [16000, 9000], 1.5, 8.0, 0.0),           # 2 warps per head
     (16, 1, 128, 16, 32768, [32768, 20000], 1.5, 5.0, 1.0),
-    (16, 1, 64, 16, 57600, [57000, 40], 2.0, 5.0, 1.0),            # 32 entries per thread
+    (16, 1, 64, 16, 57600, [57000, 40], 2.0, 5.0, 1.0),            # 8 warps per head
     (8, 1, 64, 16, 40000, [39990], 1.8, 2.0, 1.0),
-    (1, 1, 64, 16, 320000, [310000], 1.5, 8.0, 1.0),               # more than the cluster's registers hold
+    (2, 1, 64, 16, 160000, [160000], 1.5, 8.0, 1.0),               # 32 entries per thread
+    (1, 1, 64, 16, 320000, [310000], 1.5, 8.0, 1.0),               # more than a block's registers hold
     # one block per row: up to 128, 256 and 512 chunks, the last places and the first beyond
     (4, 2, 64, 32, 1000, [999, 33, 32, 1], 1.5, 3.0, 1.0),
     (16, 1, 128, 16, 2048, [2048, 2033, 16], 1.25, 4.0, 0.5),
