@@ -406,6 +406,37 @@ def test_small_values_beside_a_strong_key():
     _check_out(st.decode(q.cuda()), ref, err)
 
 
+@pytest.mark.parametrize("hq,hkv,d,B,lens", [(8, 2, 64, 32, [900, 0, 257, 1]), (16, 1, 128, 16, [400, 33, 0]),
+                                             (32, 2, 128, 128, [0, 500, 129]), (16, 4, 128, 64, [700] * 40 + [0, 3])])
+@pytest.mark.parametrize("gamma", [0.0, 3.0])
+def test_short_and_long_capacity(hq, hkv, d, B, lens, gamma):
+    """The same sequences in a cache just long enough (a block per pair) and in a long one (shared list and merge):
+    both within their bounds, zeros for the empty ones, and the routes the same."""
+    rng = np.random.default_rng(33)
+    b, n, page = len(lens), max(lens), 128
+    K, V, q = _bf16(rng, b, n, hkv, d), _bf16(rng, b, n, hkv, d), _bf16(rng, b, hq, d)
+    qbar = torch.from_numpy(rng.standard_normal((hkv, d)).astype(np.float32) * 0.3).cuda()
+    routes = []
+    for cap in (n, 9000):
+        st = _state(np.random.default_rng(34), b, cap, hq, hkv, d, chunk=B, page=page, gamma=gamma)
+        st.qbar = qbar   # (_state draws the table first, which depends on the capacity)
+        T = cap // B
+        rt = [torch.zeros(b, hkv, dtype=torch.int32, device="cuda"), torch.zeros(b, hkv, T, dtype=torch.int32, device="cuda"),
+              torch.zeros(b, hkv, T, device="cuda")]
+        if gamma:
+            st.route = D.route_out(*rt)
+        st.fill(K.cuda(), V.cuda(), lens)
+        o = st.decode(q.cuda())
+        route = [t.cpu().numpy() for t in rt] if gamma else None
+        ref, err = _decode_ref(st, q.double().numpy(), K.double().numpy(), V.double().numpy(), lens, hq, hkv, d, B, route, 0, 0)
+        _check_out(o, ref, err)
+        assert all(not o[i].any() for i, m in enumerate(lens) if m == 0)
+        if gamma:
+            routes.append([set(route[1][i, r, :route[0][i, r]]) for i in range(b) for r in range(hkv)])
+    if gamma:   # the two ways of routing round differently: a chunk at the threshold may change sides
+        assert sum(x != y for x, y in zip(*routes)) <= max(1, len(routes[0]) // 20)
+
+
 def test_steps_graph_and_streams():
     """append + decode replayed from a graph over page and chunk borders equals eager steps; a call on another stream
     gives the same; two captured graphs of two caches do not disturb each other."""
