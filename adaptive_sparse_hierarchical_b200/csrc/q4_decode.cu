@@ -77,7 +77,6 @@ struct Attend {
     float* part;      // [block][first, last][g][D + 2]: partial o, reference, sum
     int2* span;       // [pairs]: first and last block of each pair (0, -1: no granules)
     __nv_bfloat16* O;
-    int solo;         // block x has pair x to itself: nothing to merge
 };
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1)
@@ -137,7 +136,8 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 // Length of sequence b as the kernels use it.
 __device__ __forceinline__ int len_of(const Shape& s, const int* seqlens, int b) { return min(max(seqlens[b], 0), s.n); }
 
-template <int D, int NT, int U>
+// SOLO: block x has pair x to itself, there is nothing to merge.
+template <int D, int NT, int U, bool SOLO>
 __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_kernel(Shape s, Q4 c, Routes rt, Attend a)
 {
     constexpr int W = Cfg<NT>::W, NG = D / kGrp, MT = D / 16;
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
         const int full = L > 0 ? (a.dense ? (L - 1) / s.B : rt.counts[x]) : 0;
         return L > 0 ? full * NB + ((L - 1) % s.B) / kGran + 1 : 0;
     };
-    if (a.solo) {
+    if constexpr (SOLO) {
         const int x = blockIdx.x, n = granules(x);
         if (n == 0) {   // an empty sequence: zeros
             __nv_bfloat16* o = a.O + ((long long)(x / s.hkv) * s.hq + x % s.hkv * G) * D;
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
         for (int x = threadIdx.x; x < BR; x += 32 * W) pre[x + 1] = granules(x);
     }
     __syncthreads();
-    if (warp == 0 && !a.solo) {
+    if (!SOLO && warp == 0) {
         auto scan = [&](int* v, auto f) {   // v[x + 1] = f(0) + .. + f(x), v[0] = 0; returns the sum
             int run = 0;
             for (int x0 = 0; x0 < BR; x0 += 32) {
@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
             range[2] = x;
         }
     }
-    if (!a.solo) __syncthreads();
-    if (blockIdx.x == 0 && !a.solo)
+    if (!SOLO) __syncthreads();
+    if (!SOLO && blockIdx.x == 0)
         for (int x = threadIdx.x; x < BR; x += 32 * W)
             if (pre[x] == pre[x + 1]) a.span[x] = make_int2(0, -1);
     const int lo = range[0], hi = range[1];
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
             tot_l[h] = sum;
         }
         __syncthreads();
-        const bool whole = s_lo == p0 && s_hi == p1;
+        const bool whole = SOLO || (s_lo == p0 && s_hi == p1);
         float* pb = a.part + ((long long)blockIdx.x * 2 + (s_lo > p0 ? 0 : 1)) * G * (D + 2);
         for (int v = threadIdx.x; v < G * (D / 4); v += 32 * W) {
             const int h = v / (D / 4), dd = v % (D / 4) * 4;
@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
                 *reinterpret_cast<float2*>(row + 2) = make_float2(t.z, t.w);
             }
         }
-        if (threadIdx.x == 0 && !a.solo) {
+        if (!SOLO && threadIdx.x == 0) {
             if (s_lo == p0) a.span[x].x = blockIdx.x;
             if (s_hi == p1) a.span[x].y = blockIdx.x;
         }
@@ -752,22 +752,28 @@ __global__ void __launch_bounds__(D * kMergeY) q4_merge_kernel(Shape s, Attend a
     }
 }
 
-template <int D, int NT, int U>
-cudaError_t attend_t(const Shape& s, const Q4& c, const Routes& rt, Attend a, cudaStream_t st)
+template <int D, int NT, int U, bool SOLO>
+cudaError_t attend_k(const Shape& s, const Q4& c, const Routes& rt, const Attend& a, int blocks, cudaStream_t st)
 {
-    auto k = q4_attend_kernel<D, NT, U>;
+    auto k = q4_attend_kernel<D, NT, U, SOLO>;
     const size_t smem = (size_t)Cfg<NT>::W * (Stage<D, U>::N * Stage<D, U>::BYTES + sizeof(Meta));
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    return e != cudaSuccess ? e : launch_after(k, dim3(blocks), dim3(32 * Cfg<NT>::W), smem, st, s, c, rt, a);
+}
+
+template <int D, int NT, int U>
+cudaError_t attend_t(const Shape& s, const Q4& c, const Routes& rt, const Attend& a, cudaStream_t st)
+{
     const int pairs = s.batch * s.hkv, blocks = Cfg<NT>::BLOCKS * dec_tma_blocks();
     // Short caches: a block per pair, and no second kernel.  A round of a block's warps takes 0.6 (D = 64) to 1.1 us,
     // the merge and its launch 2 to 3, and the other blocks could have shared the rounds.  D = 64, 6 pairs: 500
     // tokens 7.9 -> 5.6 us a call, 1000 8.5 -> 6.9, but 2000 8.8 -> 9.3; D = 128, 6 pairs: 1000 9.6 -> 9.0, but 2000
     // 9.9 -> 13.2; 192 pairs: 2000 25.8 -> 20.3.  The limit of 16 bounds what lengths that differ can cost.
     const long long cost = (s.n + Cfg<NT>::W * 16 * U - 1ll) / (Cfg<NT>::W * 16 * U) * (D / 64);
-    a.solo = pairs <= blocks && cost <= 16 && cost * (blocks - pairs) <= 7 * blocks;
-    e = launch_after(k, dim3(a.solo ? pairs : blocks), dim3(32 * Cfg<NT>::W), smem, st, s, c, rt, a);
-    if (e != cudaSuccess || a.solo) return e;
+    if (pairs <= blocks && cost <= 16 && cost * (blocks - pairs) <= 7 * blocks)
+        return attend_k<D, NT, U, true>(s, c, rt, a, pairs, st);
+    const cudaError_t e = attend_k<D, NT, U, false>(s, c, rt, a, blocks, st);
+    if (e != cudaSuccess) return e;
     return launch_after(q4_merge_kernel<D>, dim3(pairs, pairs * s.g <= 1024 ? s.g : 1), dim3(D * kMergeY), 0, st, s, a, c.vexp);
 }
 
@@ -787,7 +793,7 @@ size_t q4_part_floats(const Shape& s) { return (size_t)2 * dec_tma_blocks() * 2 
 cudaError_t launch_attend_q4(const Shape& s, const Q4& c, const void* q, const int* seqlens, const Routes& rt, bool dense,
                              float* part, int* span, void* O, cudaStream_t st)
 {
-    const Attend a{(const __nv_bfloat16*)q, seqlens, dense ? 1 : 0, part, reinterpret_cast<int2*>(span), (__nv_bfloat16*)O, 0};
+    const Attend a{(const __nv_bfloat16*)q, seqlens, dense ? 1 : 0, part, reinterpret_cast<int2*>(span), (__nv_bfloat16*)O};
     return s.d == 128 ? attend_d<128>(s, c, rt, a, st) : attend_d<64>(s, c, rt, a, st);
 }
 
