@@ -32,12 +32,16 @@
 //   normals.  The reference moves only when a logit exceeds it by more than 6, or when room shrinks.
 //
 // Bound: 17/32 bytes of HBM per element are few enough for the unpacking to count: per 16 tokens of 128
-// elements a warp issues about 70 mask, conversion and fp32 instructions for K, 95 for V, 17 MMAs per 8 heads, the softmax.
-// Measured (L2 flushed): 48 pairs of 50021 tokens and fewer, 8 heads, all of it 283 MB: 67.9 us a call, 4.2
-// TB/s, 60% of the issue slots, 54% of the integer pipe's and 27% of the tensor pipe's cycles (the mix of integer
-// and f16 instructions alone issues at most 2.6 a cycle and SM, 65% of the slots).  16 pairs of 131072 tokens,
-// 16 heads, a quarter routed, 91 MB: 42 us of a call's 60.6, of which some 10 us are the start, the merges and the
-// second pair of a block.  Three sequences of 777 tokens and fewer: 16.5 us in four launches.
+// elements and 8 heads a warp issues some 260 instructions, of them 56 masks, 16 shifts and permutations, 14
+// conversions (all integer pipe), 19 MMAs, and 25 for the copies and their addresses.
+// Measured (L2 flushed): 48 pairs of 50021 tokens and fewer, 8 heads, all of it 283 MB: 60 us a call in short runs
+// (4.7 TB/s, 72% of a copy; 58% of the issue slots, 56% of the integer pipe's and 34% of the tensor pipe's
+// cycles), 64 to 66 in long ones, where the GPU's 1000 W hold the clock at 1.8 GHz.  A kernel without its loads takes
+// 2 us less: it is the instructions.  16 pairs of 131072 tokens, 16 heads, a quarter routed, 91 MB: 35.6 us of a
+// call's 54.5, some 7 of them the start and the merge.  Three sequences of 777 tokens and fewer: 9.8 us a call.
+// The values' scales on the weights' side instead of in every operand, with rows of one group per tile: 2% with
+// the copies as they were, 8% with what it made possible (the byte permutation, two conversions at once).  No
+// gain: shifts as multiplications (FMA pipe), 16 warps in one block, shares weighted by a block's place on its SM.
 #include <cuda_fp16.h>
 
 #include "q4.cuh"
@@ -57,7 +61,7 @@ struct Meta {
 };
 
 // Eight warps per block and as many blocks per SM as the registers of NT head tiles allow (128 and 255 per
-// thread).  Two blocks merge and start at different times: 69 us against 70 with one block of 16 warps.
+// thread).  Two blocks merge and start at different times; one block of 16 warps is as fast.
 template <int NT> struct Cfg { static constexpr int W = 8, BLOCKS = NT == 1 ? 2 : 1; };
 
 // Granules of 16 U tokens (U = 2 wherever the chunk allows: descriptors, waits and votes are paid once for
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
             }
         } else if (blk < used) {
             // Even shares of the list, in which a pair starts with kPad granules that stand for that cost (four
-            // rounds; two to five measure alike, none costs 3 to 4 us in the two large cases above).
+            // rounds; three to five measure alike in the two large cases above, two 1 us more, none 3 to 4).
             constexpr int kPad = 4 * W;
             const int all = scan(at, [&](int x) { return pre[x + 1] > pre[x] ? pre[x + 1] - pre[x] + kPad : 0; });
             const int share = all / used, more = all - share * used;
