@@ -11,8 +11,10 @@ cudaError_t launch_append_q4(const Shape& s, const Q4& c, const void* K, const v
                              const float* qbar, float* kbar, float* state, int* seqlens, cudaStream_t st);
 cudaError_t launch_load_q4(const Shape& s, const Q4& c, const int* start, int offset, int n, const int* seqlens,
                            void* K, void* V, cudaStream_t st);
-cudaError_t launch_attend_q4(const Shape& s, const Q4& c, const void* q, const int* seqlens, const Routes& rt, bool dense,
-                             float* part, int* span, void* O, cudaStream_t st);
+// kbar: the summaries, for caches whose blocks route their pairs themselves (q4_solo); else null
+cudaError_t launch_attend_q4(const Shape& s, const Q4& c, const void* q, const int* seqlens, const float* kbar,
+                             const Routes& rt, bool dense, float* part, int* span, void* O, cudaStream_t st);
+bool q4_solo(const Shape& s);
 bool route_q4_supported(const Shape& s);
 cudaError_t launch_route_q4(const Shape& s, const void* q, const float* kbar, const int* seqlens, const Routes& rt,
                             float* X, int* status, cudaStream_t st);
@@ -214,7 +216,8 @@ int dash_decode_q4(const dash_params* p, const dash_q4_kv* kv, const void* q, co
     rt.cap = s.T;
     rt.words = (s.T + 31) / 32;
     if (!on(rt.counts, 4) || !on(rt.idx, 4) || !on(rt.bias, 4) || !on(rt.bitmask, 4)) return DASH_EALIGN;
-    if (routed) {
+    const bool ahead = routed && !q4_solo(s);   // routing in launches of its own
+    if (ahead) {
         float* X = (float*)(ws + L.x);
         int* err = (int*)(ws + L.err);
         rc = status_of(route_q4_supported(s)
@@ -226,8 +229,8 @@ int dash_decode_q4(const dash_params* p, const dash_q4_kv* kv, const void* q, co
         const size_t bh = (size_t)p->batch * p->h_kv;
         if ((rc = status_of(cudaMemsetAsync(rt.counts, 0, bh * 4, (cudaStream_t)stream))) != DASH_OK) return rc;
     }
-    return status_of(launch_attend_q4(s, cache_of(kv), q, seqlens, rt, dense, (float*)(ws + L.part), (int*)(ws + L.span), O,
-                                      (cudaStream_t)stream));
+    return status_of(launch_attend_q4(s, cache_of(kv), q, seqlens, routed && !ahead ? kbar_cache : nullptr, rt, dense,
+                                      (float*)(ws + L.part), (int*)(ws + L.span), O, (cudaStream_t)stream));
 }
 
 size_t dash_pages_workspace_size(const dash_pages* pg)

@@ -44,13 +44,13 @@
 // gain: shifts as multiplications (FMA pipe), 16 warps in one block, shares weighted by a block's place on its SM.
 #include <cuda_fp16.h>
 
-#include "q4.cuh"
-#include "stage2_mma.cuh"
+#include "q4_route.cuh"
 
 namespace dash {
 namespace {
 
 constexpr int kMaxPairs = 2048;
+constexpr int kSoloWords = 4;     // a block that has a pair to itself: at most 128 chunks (see q4_solo)
 constexpr int kMeta = 64;         // granule descriptors per warp (two halves of 32)
 
 // Descriptor of a granule: where its codes and scales lie, its chunk's bias, tokens | mapped << 8.
@@ -81,6 +81,7 @@ struct Attend {
     float* part;      // [block][first, last][g][D + 2]: partial o, reference, sum
     int2* span;       // [pairs]: first and last block of each pair (0, -1: no granules)
     __nv_bfloat16* O;
+    const float* kbar;   // SOLO: the summaries, where the block routes its pair itself (else null)
 };
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1)
@@ -140,7 +141,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 // Length of sequence b as the kernels use it.
 __device__ __forceinline__ int len_of(const Shape& s, const int* seqlens, int b) { return min(max(seqlens[b], 0), s.n); }
 
-// SOLO: block x has pair x to itself, there is nothing to merge.
+// SOLO: block x has pair x to itself: it routes it first, and there is nothing to merge.
 template <int D, int NT, int U, bool SOLO>
 __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_kernel(Shape s, Q4 c, Routes rt, Attend a)
 {
@@ -167,7 +168,13 @@ __global__ void __launch_bounds__(32 * Cfg<NT>::W, Cfg<NT>::BLOCKS) q4_attend_ke
         return L > 0 ? full * NB + ((L - 1) % s.B) / kGran + 1 : 0;
     };
     if constexpr (SOLO) {
-        const int x = blockIdx.x, n = granules(x);
+        const int x = blockIdx.x;
+        if (a.kbar) {
+            float* scratch = reinterpret_cast<float*>(smem);   // 16 rows of 132 logits, 8 sums: the rings come later
+            route_row<D, kSoloWords>(s, a.q, a.kbar, rt, x, chunks_of(s, a.seqlens, x / s.hkv), scratch, scratch + 16 * 132);
+            __syncthreads();   // the routes are there, the scratch is free
+        }
+        const int n = granules(x);
         if (n == 0) {   // an empty sequence: zeros
             __nv_bfloat16* o = a.O + ((long long)(x / s.hkv) * s.hq + x % s.hkv * G) * D;
             for (int v = threadIdx.x; v < G * D / 8; v += 32 * W) reinterpret_cast<uint4*>(o)[v] = make_uint4(0u, 0u, 0u, 0u);
@@ -756,6 +763,24 @@ __global__ void __launch_bounds__(D * kMergeY) q4_merge_kernel(Shape s, Attend a
     }
 }
 
+}  // namespace
+
+// Short caches: a block per pair, which routes and attends in one launch.  A round of a block's warps takes 0.6 (D =
+// 64) to 1.1 us, the merge and its launch 2 to 3, and the other blocks could have shared the rounds.  Dense, D = 64,
+// 6 pairs: 500 tokens 7.9 -> 5.6 us a call, 1000 8.5 -> 6.9, but 2000 8.8 -> 9.3; D = 128, 6 pairs: 1000 9.6 ->
+// 9.0, but 2000 9.9 -> 13.2; 192 pairs: 2000 25.8 -> 20.3.  The limit of 16 bounds what lengths that differ can
+// cost, and the chunks: 4096 tokens in chunks of 32 or more, 2048 in chunks of 16.
+bool q4_solo(const Shape& s)
+{
+    static_assert(Cfg<1>::W == 8 && Cfg<2>::W == 8 && kSoloWords * 32 >= 16 * 8 * 32 / 32 && kSoloWords * 32 >= 16 * 8 * 16 / 16,
+                  "the routing of a block takes all chunks");
+    const long long round = 8 * (s.B % 32 == 0 ? 32 : 16), cost = (s.n + round - 1) / round * (s.d / 64);
+    const int pairs = s.batch * s.hkv, blocks = (s.g <= 8 ? Cfg<1>::BLOCKS : Cfg<2>::BLOCKS) * dec_tma_blocks();
+    return pairs <= blocks && cost <= 16 && cost * (blocks - pairs) <= 7 * blocks;
+}
+
+namespace {
+
 template <int D, int NT, int U, bool SOLO>
 cudaError_t attend_k(const Shape& s, const Q4& c, const Routes& rt, const Attend& a, int blocks, cudaStream_t st)
 {
@@ -769,13 +794,7 @@ template <int D, int NT, int U>
 cudaError_t attend_t(const Shape& s, const Q4& c, const Routes& rt, const Attend& a, cudaStream_t st)
 {
     const int pairs = s.batch * s.hkv, blocks = Cfg<NT>::BLOCKS * dec_tma_blocks();
-    // Short caches: a block per pair, and no second kernel.  A round of a block's warps takes 0.6 (D = 64) to 1.1 us,
-    // the merge and its launch 2 to 3, and the other blocks could have shared the rounds.  D = 64, 6 pairs: 500
-    // tokens 7.9 -> 5.6 us a call, 1000 8.5 -> 6.9, but 2000 8.8 -> 9.3; D = 128, 6 pairs: 1000 9.6 -> 9.0, but 2000
-    // 9.9 -> 13.2; 192 pairs: 2000 25.8 -> 20.3.  The limit of 16 bounds what lengths that differ can cost.
-    const long long cost = (s.n + Cfg<NT>::W * 16 * U - 1ll) / (Cfg<NT>::W * 16 * U) * (D / 64);
-    if (pairs <= blocks && cost <= 16 && cost * (blocks - pairs) <= 7 * blocks)
-        return attend_k<D, NT, U, true>(s, c, rt, a, pairs, st);
+    if (q4_solo(s)) return attend_k<D, NT, U, true>(s, c, rt, a, pairs, st);
     const cudaError_t e = attend_k<D, NT, U, false>(s, c, rt, a, blocks, st);
     if (e != cudaSuccess) return e;
     return launch_after(q4_merge_kernel<D>, dim3(pairs, pairs * s.g <= 1024 ? s.g : 1), dim3(D * kMergeY), 0, st, s, a, c.vexp);
@@ -794,10 +813,11 @@ int q4_max_pairs() { return kMaxPairs; }
 
 size_t q4_part_floats(const Shape& s) { return (size_t)2 * dec_tma_blocks() * 2 * s.g * (s.d + 2); }
 
-cudaError_t launch_attend_q4(const Shape& s, const Q4& c, const void* q, const int* seqlens, const Routes& rt, bool dense,
-                             float* part, int* span, void* O, cudaStream_t st)
+cudaError_t launch_attend_q4(const Shape& s, const Q4& c, const void* q, const int* seqlens, const float* kbar,
+                             const Routes& rt, bool dense, float* part, int* span, void* O, cudaStream_t st)
 {
-    const Attend a{(const __nv_bfloat16*)q, seqlens, dense ? 1 : 0, part, reinterpret_cast<int2*>(span), (__nv_bfloat16*)O};
+    const Attend a{(const __nv_bfloat16*)q, seqlens, dense ? 1 : 0, part, reinterpret_cast<int2*>(span), (__nv_bfloat16*)O,
+                   kbar};
     return s.d == 128 ? attend_d<128>(s, c, rt, a, st) : attend_d<64>(s, c, rt, a, st);
 }
 
