@@ -14,7 +14,7 @@ cudaError_t launch_load_q4(const Shape& s, const Q4& c, const int* start, int of
 // kbar: the summaries, for caches whose blocks route their pairs themselves (q4_solo); else null
 cudaError_t launch_attend_q4(const Shape& s, const Q4& c, const void* q, const int* seqlens, const float* kbar,
                              const Routes& rt, bool dense, float* part, int* span, void* O, cudaStream_t st);
-bool q4_solo(const Shape& s);
+bool q4_solo(const Shape& s, bool routed);
 bool route_q4_supported(const Shape& s);
 cudaError_t launch_route_q4(const Shape& s, const void* q, const float* kbar, const int* seqlens, const Routes& rt,
                             float* X, int* status, cudaStream_t st);
@@ -216,7 +216,7 @@ int dash_decode_q4(const dash_params* p, const dash_q4_kv* kv, const void* q, co
     rt.cap = s.T;
     rt.words = (s.T + 31) / 32;
     if (!on(rt.counts, 4) || !on(rt.idx, 4) || !on(rt.bias, 4) || !on(rt.bitmask, 4)) return DASH_EALIGN;
-    const bool ahead = routed && !q4_solo(s);   // routing in launches of its own
+    const bool ahead = routed && !q4_solo(s, !dense);   // routing in launches of its own
     if (ahead) {
         float* X = (float*)(ws + L.x);
         int* err = (int*)(ws + L.err);

@@ -768,15 +768,18 @@ __global__ void __launch_bounds__(D * kMergeY) q4_merge_kernel(Shape s, Attend a
 // Short caches: a block per pair, which routes and attends in one launch.  A round of a block's warps takes 0.6 (D =
 // 64) to 1.1 us, the merge and its launch 2 to 3, and the other blocks could have shared the rounds.  Dense, D = 64,
 // 6 pairs: 500 tokens 7.9 -> 5.6 us a call, 1000 8.5 -> 6.9, but 2000 8.8 -> 9.3; D = 128, 6 pairs: 1000 9.6 ->
-// 9.0, but 2000 9.9 -> 13.2; 192 pairs: 2000 25.8 -> 20.3.  The limit of 16 bounds what lengths that differ can
-// cost, and the chunks: 4096 tokens in chunks of 32 or more, 2048 in chunks of 16.
-bool q4_solo(const Shape& s)
+// 9.0, but 2000 9.9 -> 13.2; 192 pairs: 2000 25.8 -> 20.3.  Routed calls save the routing's launches too, and walk
+// some of the chunks: D = 64, 6 pairs: 2000 tokens 13.2 -> 8.4, 3500 13.7 -> 9.2; D = 128: 1750 14.5 -> 10.1, but with
+// 16 heads (rounds a quarter longer) 17.2 -> 19.5.  The limit of 16 bounds what lengths that differ can cost, and the
+// chunks: 4096 tokens in chunks of 32 or more, 2048 in chunks of 16.
+bool q4_solo(const Shape& s, bool routed)
 {
     static_assert(Cfg<1>::W == 8 && Cfg<2>::W == 8 && kSoloWords * 32 >= 16 * 8 * 32 / 32 && kSoloWords * 32 >= 16 * 8 * 16 / 16,
                   "the routing of a block takes all chunks");
-    const long long round = 8 * (s.B % 32 == 0 ? 32 : 16), cost = (s.n + round - 1) / round * (s.d / 64);
+    const long long round = 8 * (s.B % 32 == 0 ? 32 : 16), rounds = (s.n + round - 1) / round;
+    const long long cost = rounds * (s.d / 64) + (s.g > 8 ? rounds * (s.d / 64) / 4 : 0);
     const int pairs = s.batch * s.hkv, blocks = (s.g <= 8 ? Cfg<1>::BLOCKS : Cfg<2>::BLOCKS) * dec_tma_blocks();
-    return pairs <= blocks && cost <= 16 && cost * (blocks - pairs) <= 7 * blocks;
+    return pairs <= blocks && cost <= 16 && (routed || cost * (blocks - pairs) <= 7 * blocks);
 }
 
 namespace {
@@ -794,7 +797,7 @@ template <int D, int NT, int U>
 cudaError_t attend_t(const Shape& s, const Q4& c, const Routes& rt, const Attend& a, cudaStream_t st)
 {
     const int pairs = s.batch * s.hkv, blocks = Cfg<NT>::BLOCKS * dec_tma_blocks();
-    if (q4_solo(s)) return attend_k<D, NT, U, true>(s, c, rt, a, pairs, st);
+    if (q4_solo(s, !a.dense)) return attend_k<D, NT, U, true>(s, c, rt, a, pairs, st);
     const cudaError_t e = attend_k<D, NT, U, false>(s, c, rt, a, blocks, st);
     if (e != cudaSuccess) return e;
     return launch_after(q4_merge_kernel<D>, dim3(pairs, pairs * s.g <= 1024 ? s.g : 1), dim3(D * kMergeY), 0, st, s, a, c.vexp);
