@@ -9,7 +9,8 @@
 // list that the blocks share evenly; a block's warps take its granules in turn, each with its own
 // online softmax and its own ring of cp.async stages (a granule is used by one warp only, so no
 // barrier is involved), and merge at the end of a pair.  A pair inside one block is finished there;
-// pieces of a pair that spans blocks are merged by a second kernel, in block order.
+// pieces of a pair that spans blocks are merged by a second kernel, in block order.  Short caches give each pair a
+// block of its own, which routes the pair as well (SOLO).
 //
 // A warp computes S^T = K q^T and O^T = V^T P^T: 16 tokens (then 16 of the d_h elements) are the
 // 16 rows of m16n8k16 MMAs and the heads the 8 columns, so groups of up to 8 heads fill the tile.
@@ -38,7 +39,8 @@
 // (4.7 TB/s, 72% of a copy; 58% of the issue slots, 56% of the integer pipe's and 34% of the tensor pipe's
 // cycles), 64 to 66 in long ones, where the GPU's 1000 W hold the clock at 1.8 GHz.  A kernel without its loads takes
 // 2 us less: it is the instructions.  16 pairs of 131072 tokens, 16 heads, a quarter routed, 91 MB: 35.6 us of a
-// call's 54.5, some 7 of them the start and the merge.  Three sequences of 777 tokens and fewer: 9.8 us a call.
+// call's 54.4, some 7 of them the start and the merge.  Three sequences of 777 tokens and fewer, routed: 7.8 us a
+// call, one launch.
 // The values' scales on the weights' side instead of in every operand, with rows of one group per tile: 2% with
 // the copies as they were, 8% with what it made possible (the byte permutation, two conversions at once).  No
 // gain: shifts as multiplications (FMA pipe), 16 warps in one block, shares weighted by a block's place on its SM.

@@ -13,7 +13,8 @@
 //      block barrier.  The weights take the logits' place (in L2);
 //   3. in a cluster of 4 blocks per pair each block adds up the heads' weights for a quarter of the chunks, and
 //      the blocks tell each other their counts and sums of logarithms.
-// Short rows take one block and one launch instead (route_short_kernel).
+// Short rows take one block and one launch instead (route_short_kernel; in the shortest caches the attending block
+// does it, see q4_decode.cu).
 // Measured: with cold caches 16 pairs of 2047 chunks and 16 heads of 128 take 10 us for the logits (16.8 MB, 1.7
 // TB/s: a read of this size is latency); one cluster for everything takes 25 to 26 us there.  Whole calls: steps 2
 // and 3 in one kernel, with the heads spread over the cluster's blocks, are 1 us slower there (36.3 against
