@@ -199,8 +199,8 @@ int dash_decode_q4(const dash_params* p, const dash_q4_kv* kv, const void* q, co
     if (!on(q, 16) || !on(O, 16) || !on(kbar_cache, 16) || !on(seqlens, 4)) return DASH_EALIGN;
     if ((long long)p->batch * p->h_kv > q4_max_pairs()) return DASH_EUNSUPPORTED;
     const Shape s = shape_of(p);
-    // the pairs' granules (16 tokens or more) are numbered in 32 bits
-    if ((long long)p->batch * p->h_kv * (p->seqlen / 16 + 1ll) > 0x7fffffffll) return DASH_EUNSUPPORTED;
+    // the pairs' granules (16 tokens or more), and what stands for a pair's start, are numbered in 32 bits
+    if ((long long)p->batch * p->h_kv * (p->seqlen / 16 + 33ll) > 0x7fffffffll) return DASH_EUNSUPPORTED;
     // where the routing of q4_route.cu stops, Stage 1 keeps every head's logits of one (sequence, KV head) in shared
     // memory
     if (routed && !route_q4_supported(s) && (size_t)s.g * (size_t)s.T * 4 > 225 * 1024) return DASH_EUNSUPPORTED;

@@ -17,9 +17,10 @@ __device__ __forceinline__ void split3(float2 x, uint32_t& hi, uint32_t& mid, ui
     lo = __byte_perm(__float_as_uint(r0 - m0), __float_as_uint(r1 - m1), 0x7632);
 }
 
+// Complete chunks before the query's own (a length beyond the capacity counts as the capacity).
 __device__ __forceinline__ int chunks_of(const Shape& s, const int* seqlens, int b)
 {
-    return max(0, min((seqlens[b] - 1) / s.B, s.T));
+    return max(0, (min(seqlens[b], s.n) - 1) / s.B);
 }
 
 // The chunks' summaries of one 8-chunk tile: this lane's elements of chunk g8 (on: it is there).

@@ -463,6 +463,18 @@ def test_steps_graph_and_streams():
         assert torch.equal(getattr(eager, name), getattr(other, name)), name
 
 
+@pytest.mark.parametrize("cap", [256, 9984])
+def test_length_beyond_the_capacity(cap):
+    """A length that someone set too large counts as the capacity: no chunk is attended twice."""
+    rng = np.random.default_rng(35)
+    K, V, q = _bf16(rng, 2, cap, 2, 64), _bf16(rng, 2, cap, 2, 64), _bf16(rng, 2, 4, 64)
+    st = _state(rng, 2, cap, 4, 2, 64, chunk=32, page=64, gamma=2.0)
+    st.fill(K.cuda(), V.cuda(), [cap, cap])
+    o = st.decode(q.cuda()).clone()
+    st.seqlens += torch.tensor([1, 10 ** 6], dtype=torch.int32, device="cuda")
+    assert torch.equal(st.decode(q.cuda()), o)
+
+
 def test_graph_refuses_other_shapes():
     """A recorded step takes the sizes and type it was recorded with: nothing is broadcast or converted."""
     rng = np.random.default_rng(28)
