@@ -201,9 +201,7 @@ int dash_decode_q4(const dash_params* p, const dash_q4_kv* kv, const void* q, co
     const Shape s = shape_of(p);
     // the pairs' granules (16 tokens or more), and what stands for a pair's start, are numbered in 32 bits
     if ((long long)p->batch * p->h_kv * (p->seqlen / 16 + 33ll) > 0x7fffffffll) return DASH_EUNSUPPORTED;
-    // where the routing of q4_route.cu stops, Stage 1 keeps every head's logits of one (sequence, KV head) in shared
-    // memory
-    if (routed && !route_q4_supported(s) && (size_t)s.g * (size_t)s.T * 4 > 225 * 1024) return DASH_EUNSUPPORTED;
+    if (routed && !route_q4_supported(s)) return DASH_EUNSUPPORTED;
     const Q4Layout L = q4_layout(p);
     if (!workspace || ws_bytes < L.total) return DASH_EWORKSPACE;
     if (!on(workspace, kAlign)) return DASH_EALIGN;
@@ -220,9 +218,7 @@ int dash_decode_q4(const dash_params* p, const dash_q4_kv* kv, const void* q, co
     if (ahead) {
         float* X = (float*)(ws + L.x);
         int* err = (int*)(ws + L.err);
-        rc = status_of(route_q4_supported(s)
-                           ? launch_route_q4(s, q, kbar_cache, seqlens, rt, X, err, (cudaStream_t)stream)
-                           : launch_route_decode(s, p->dtype, q, kbar_cache, s.T, seqlens, rt, X, err, (cudaStream_t)stream));
+        rc = status_of(launch_route_q4(s, q, kbar_cache, seqlens, rt, X, err, (cudaStream_t)stream));
         if (rc != DASH_OK) return rc;
     }
     if (none && route) {

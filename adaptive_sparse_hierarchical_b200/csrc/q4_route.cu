@@ -30,7 +30,7 @@ namespace dash {
 namespace {
 
 constexpr int kLogitWarps = 8, kTiles = 2;   // 8-chunk tiles per warp
-constexpr int kCl = 4, kThr = 512, kWarps = kThr / 32, kMaxVals = 32;
+constexpr int kCl = 4, kThr = 512, kWarps = kThr / 32, kMaxVals = 32, kLong = 8;
 
 // X [pair][head][T]: the logits of the complete chunks before each query's own.
 template <int D>
@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(32 * kLogitWarps) route_logits_kernel(Shape s,
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3, G = s.g;
     const unsigned per = (s.T + 8 * kTiles - 1) / (8 * kTiles);
-    const unsigned unit = blockIdx.x * kLogitWarps + warp;   // at most 2048 pairs x 16384 chunks / 16
+    const unsigned unit = blockIdx.x * kLogitWarps + warp;   // at most 2048 pairs x 57600 chunks / 16
     if (unit >= (unsigned)(s.batch * s.hkv) * per) return;
     const int br = unit / per, c0 = (unit % per) * 8 * kTiles, b = br / s.hkv, r = br % s.hkv;
     const int nv = chunks_of(s, seqlens, b);
@@ -85,7 +85,8 @@ inline int warps_per_head(int T)
 // Chunks per block in the last phase: whole 32-chunk words.
 __host__ __device__ inline int quarter(int nv) { return ((nv + kCl - 1) / kCl + 31) / 32 * 32; }
 
-// Thresholds: a block per (pair, head).  The head's weights [x - tau]_+^p take its logits' place in X.
+// Thresholds: a block per (pair, head).  The head's weights [x - tau]_+^p take its logits' place in X.  V: entries per
+// thread, held in registers; 0: rows of any length, read again (from L1 and L2) at every step, kLong at a time.
 template <int V>
 __global__ void __launch_bounds__(kThr) route_tau_kernel(Shape s, float* X, const int* __restrict__ seqlens, int* status)
 {
@@ -99,12 +100,33 @@ __global__ void __launch_bounds__(kThr) route_tau_kernel(Shape s, float* X, cons
     if (nv == 0) return;
     const float p = 1.f / (s.alpha - 1.f);
     const int mode = ent_mode(s.alpha);
-    float v[V], mx = -INFINITY;
+    constexpr int N = V ? V : kLong;
+    float v[N], mx = -INFINITY;
     float* row = X + (long long)blockIdx.x * s.T;
+    auto load = [&](int c0) {
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-        v[k] = tid + k * step < nv ? row[tid + k * step] : -INFINITY;
-        mx = fmaxf(mx, v[k]);
+        for (int k = 0; k < N; ++k) v[k] = c0 + k * step < nv ? row[c0 + k * step] : -INFINITY;
+    };
+    auto relative = [&] {
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] -= mx;
+    };
+    // f on every part of the row, less its maximum (one part where it is in registers)
+    auto parts = [&](auto f) {
+        if constexpr (V != 0) {
+            f(tid);
+        } else {
+            for (int c0 = tid; c0 < nv; c0 += N * step) {
+                load(c0);
+                relative();
+                f(c0);
+            }
+        }
+    };
+    for (int c0 = tid; c0 < (V ? tid + 1 : nv); c0 += N * step) {
+        load(c0);
+#pragma unroll
+        for (int k = 0; k < N; ++k) mx = fmaxf(mx, v[k]);
     }
     mx = warp_max(mx);
     if (warps > 1) {
@@ -112,11 +134,13 @@ __global__ void __launch_bounds__(kThr) route_tau_kernel(Shape s, float* X, cons
         __syncthreads();
         for (int k = 0; k < warps; ++k) mx = fmaxf(mx, red[k]);
     }
-    // Newton steps from max - 1, at most one barrier each
-    float lo = mx - 1.f, t = lo, hi = mx - exp2f(-(s.alpha - 1.f) * __log2f((float)nv));
+    if constexpr (V != 0) relative();
+    // Newton steps from the maximum - 1, at most one barrier each
+    float lo, t, hi;
+    bracket(lo, t, hi, s.alpha, nv);
     for (int it = 0; it < kMaxIter; ++it) {
         float f = 0.f, fd = 0.f;
-        sums<V>(v, t, p, mode, f, fd);
+        parts([&](int) { sums<N>(v, t, p, mode, f, fd); });
         f = warp_sum(f);
         fd = warp_sum(fd);
         if (warps > 1) {
@@ -133,12 +157,14 @@ __global__ void __launch_bounds__(kThr) route_tau_kernel(Shape s, float* X, cons
         }
         if (newton(f, fd, t, lo, hi, s.alpha, mode)) break;   // the same numbers in every thread
     }
+    parts([&](int c0) {
 #pragma unroll
-    for (int k = 0; k < V; ++k)
-        if (tid + k * step < nv) {
-            const float u = fmaxf(v[k] - t, 0.f);
-            __stcg(row + tid + k * step, mode == 2 ? u * u : mode == 1 ? u : power(u, p));
-        }
+        for (int k = 0; k < N; ++k)
+            if (c0 + k * step < nv) {
+                const float u = fmaxf(v[k] - t, 0.f);
+                __stcg(row + c0 + k * step, mode == 2 ? u * u : mode == 1 ? u : power(u, p));
+            }
+    });
 }
 
 // Group weights and lists: a cluster of 4 blocks per pair, a quarter of the chunks each.
@@ -272,8 +298,8 @@ cudaError_t tau_t(const Shape& s, float* X, const int* seqlens, int* status, cud
 
 }  // namespace
 
-// A thread holds at most 32 entries (a quarter of the chunks' weights is then less than a block's shared memory).
-bool route_q4_supported(const Shape& s) { return s.T > 0 && s.T <= kMaxVals * kThr; }
+// Rows that a block's registers hold, longer ones as long as a pair's logits (the heads' rows) stay within 225 KB.
+bool route_q4_supported(const Shape& s) { return s.T > 0 && (s.T <= kMaxVals * kThr || (long long)s.g * s.T <= 57600); }
 
 cudaError_t launch_route_q4(const Shape& s, const void* q, const float* kbar, const int* seqlens, const Routes& rt,
                             float* X, int* status, cudaStream_t st)
@@ -286,10 +312,15 @@ cudaError_t launch_route_q4(const Shape& s, const void* q, const float* kbar, co
     cudaError_t e = launch_after(s.d == 128 ? route_logits_kernel<128> : route_logits_kernel<64>, grid,
                                        dim3(32 * kLogitWarps), 0, st, s, (const __nv_bfloat16*)q, kbar, seqlens, X);
     if (e != cudaSuccess) return e;
-    e = s.T <= 16 * kThr ? tau_t<16>(s, X, seqlens, status, st) : tau_t<kMaxVals>(s, X, seqlens, status, st);
+    e = s.T <= 16 * kThr         ? tau_t<16>(s, X, seqlens, status, st)
+        : s.T <= kMaxVals * kThr ? tau_t<kMaxVals>(s, X, seqlens, status, st)
+                                 : tau_t<0>(s, X, seqlens, status, st);
     if (e != cudaSuccess) return e;
-    return launch_after(route_list_kernel, dim3(kCl * s.batch * s.hkv), dim3(kThr), quarter(s.T) * 4, st, s, (const float*)X,
-                        seqlens, rt);
+    const int keep = quarter(s.T) * 4;   // at most 57.6 KB (T <= 57600)
+    if (keep > 48 * 1024 &&
+        (e = cudaFuncSetAttribute(route_list_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, keep)) != cudaSuccess)
+        return e;
+    return launch_after(route_list_kernel, dim3(kCl * s.batch * s.hkv), dim3(kThr), keep, st, s, (const float*)X, seqlens, rt);
 }
 
 }  // namespace dash
