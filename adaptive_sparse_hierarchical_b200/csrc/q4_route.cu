@@ -160,10 +160,7 @@ __global__ void __launch_bounds__(kThr) route_tau_kernel(Shape s, float* X, cons
     parts([&](int c0) {
 #pragma unroll
         for (int k = 0; k < N; ++k)
-            if (c0 + k * step < nv) {
-                const float u = fmaxf(v[k] - t, 0.f);
-                __stcg(row + c0 + k * step, mode == 2 ? u * u : mode == 1 ? u : power(u, p));
-            }
+            if (c0 + k * step < nv) __stcg(row + c0 + k * step, weight_of(v[k] - t, p, mode));
     });
 }
 
@@ -189,12 +186,13 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThr, 1)
     const float inv_g = 1.f / G;
     const float* wrow = X + (long long)br * G * s.T;
     auto weight = [&](int c) {   // the heads in order; the reads are on their way before the first is added
-        float a[16], sum = 0.f;
+        float a[16];
+        GroupWeight sum;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) a[k] = k < G ? __ldcg(wrow + (long long)k * s.T + c) : 0.f;
+        for (int k = 0; k < 16; ++k) a[k] = k < G ? __ldcg(wrow + (long long)k * s.T + c) : __int_as_float(0x7fffffff);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) sum += a[k];
-        return sum * inv_g;
+        for (int k = 0; k < 16; ++k) sum.add(a[k]);
+        return sum.mean(inv_g);
     };
     float sl = 0.f;
     int cn = 0;
@@ -202,7 +200,7 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThr, 1)
     for (int c = w_lo + lane; c < w_hi; c += 32) {
         const float w = weight(c);
         keep[c - c_lo] = w;
-        if (w > 0.f) { sl += __logf(w); ++cn; }
+        if (routed(w)) { sl += __logf(w); ++cn; }
     }
     sl = warp_sum(sl);
     cn = warp_isum(cn);
@@ -236,7 +234,7 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThr, 1)
     for (int c0 = w_lo; c0 < w_hi; c0 += 32) {
         const int c = c0 + lane;
         const float w = c < w_hi ? keep[c - c_lo] : 0.f;
-        const bool on = w > 0.f;
+        const bool on = routed(w);
         const uint32_t m = __ballot_sync(0xffffffffu, on);
         if (on) {
             const int j = at + __popc(m & ((1u << lane) - 1u));

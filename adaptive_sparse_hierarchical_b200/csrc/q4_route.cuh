@@ -48,9 +48,32 @@ __device__ __forceinline__ void tile_logits(float* acc, const uint32_t (&qf)[D /
     }
 }
 
-// u^p for u >= 0, kept out of line: alpha other than 1.5 and 2 is rare, and code that is only passed over
+// u^p for u >= 0 (or a NaN, which stays), kept out of line: alpha other than 1.5 and 2 is rare, and code that is only passed over
 // has to be fetched too (these kernels run once per call, from a cold instruction cache).
-static __device__ __noinline__ float power(float u, float p) { return u > 0.f ? exp2f(p * __log2f(u)) : 0.f; }
+static __device__ __noinline__ float power(float u, float p) { return u > 0.f ? exp2f(p * __log2f(u)) : u; }
+
+// Weight [x]_+^p of a logit x less the threshold.  The solve passes over NaNs; here they come back.
+__device__ __forceinline__ float weight_of(float x, float p, int mode)
+{
+    const float u = x < 0.f ? 0.f : x;
+    return mode == 2 ? u * u : mode == 1 ? u : power(u, p);
+}
+// A chunk's group weight, from the heads' in order.  A summary that is not finite gives every head a NaN: the weight is
+// one too, the chunk is routed, and the mean of the logarithms carries it to all of the pair's biases and outputs.  A
+// query that is not finite gives them to its own head alone, whose output they reach anyway: the others go without it.
+struct GroupWeight {
+    float sum = 0.f;
+    bool any = false;
+    __device__ __forceinline__ void add(float w)
+    {
+        if (w == w) {
+            sum += w;
+            any = true;
+        }
+    }
+    __device__ __forceinline__ float mean(float inv_g) const { return any ? sum * inv_g : __int_as_float(0x7fffffff); }
+};
+__device__ __forceinline__ bool routed(float w) { return !(w <= 0.f); }
 
 // f = sum u^p, fd = sum u^(p-1) over the entries u = v - t > 0 of this thread.
 template <int V>
@@ -160,10 +183,7 @@ __device__ __forceinline__ void route_row(const Shape& s, const __nv_bfloat16* q
             if (newton(f, fd, t, lo, hi, s.alpha, mode)) break;
         }
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const float u = fmaxf(v[k] - t, 0.f);
-            x[h * LD + lane + 32 * k] = mode == 2 ? u * u : mode == 1 ? u : power(u, p);
-        }
+        for (int k = 0; k < V; ++k) x[h * LD + lane + 32 * k] = weight_of(v[k] - t, p, mode);
     }
     __syncthreads();
 
@@ -172,11 +192,12 @@ __device__ __forceinline__ void route_row(const Shape& s, const __nv_bfloat16* q
     uint32_t m = 0;
     if (warp < V && warp * 32 < nv) {
         if (tid < nv) {
-            for (int k = 0; k < G; ++k) w += x[k * LD + tid];
-            w *= 1.f / G;
+            GroupWeight sum;
+            for (int k = 0; k < G; ++k) sum.add(x[k * LD + tid]);
+            w = sum.mean(1.f / G);
         }
-        m = __ballot_sync(0xffffffffu, w > 0.f);
-        lw = w > 0.f ? __logf(w) : 0.f;
+        m = __ballot_sync(0xffffffffu, routed(w));
+        lw = routed(w) ? __logf(w) : 0.f;
         const float sl = warp_sum(lw);
         if (lane == 0) { lsum[warp] = sl; csum[warp] = __popc(m); }
     } else if (warp < V && lane == 0) {

@@ -59,7 +59,9 @@ int dash_load_q4(const dash_params* p, const dash_q4_kv* kv, const int* start, i
  * b at position seqlens[b] - 1.  gamma = 0 attends over every cached token (dense attention, bias
  * 0); kbar_cache may then be NULL unless `route` is given (and for every call on a cache that is shorter
  * than a chunk).  A sequence of length 0 gives zeros.  batch * h_kv <= 2048; query elements up to 2^88
- * (beyond, logits of about that size overflow).  Workspace: dash_q4_workspace_size(p), 256-byte aligned. */
+ * (beyond, logits of about that size overflow).  A query that is not finite makes its head's output NaN; a chunk whose
+ * summary is not finite is routed, and makes the outputs of its KV head's group NaN.  Workspace:
+ * dash_q4_workspace_size(p), 256-byte aligned. */
 size_t dash_q4_workspace_size(const dash_params* p);
 int dash_decode_q4(const dash_params* p, const dash_q4_kv* kv, const void* q, const float* kbar_cache,
                    const int* seqlens, void* O, const dash_route_out* route, void* workspace, size_t ws_bytes,

@@ -1,4 +1,4 @@
-"""Routing of the 4-bit decode where its logits are unusual in size.  The summaries are set by
+"""Routing of the 4-bit decode where its logits are unusual: of any size, and not finite.  The summaries are set by
 hand so that every logit is a float32 number and no rounding happens before the thresholds."""
 import numpy as np
 import pytest
@@ -97,3 +97,38 @@ def test_logits_of_any_size(T, B, g, alpha, top):
         # (the device's logarithm is within 2^-21.4 absolutely, and the mean of n of them within n roundings)
         tol = 1.2 * (dl + dl.mean()) + 2 * 2.0 ** -21 + (got.sum() + 32) * 2.0 ** -24 * np.abs(lw).max()
         assert (np.abs(bias[r, :counts[r]] - (lw - lw.mean())) <= tol).all(), r
+
+
+@pytest.mark.parametrize("T,B,g", FORMS)
+@pytest.mark.parametrize("alpha", [1.5, 2.0, 1.25])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_keys_that_are_not_numbers(T, B, g, alpha, bad):
+    """A completed chunk whose summary is not finite reaches the outputs of its KV head, as the chunk's keys do
+    without routing; other heads and sequences are as without it."""
+    rng = np.random.default_rng(T)
+    d, hkv, slots = 64, 2, T + 1
+    st = D.Q4DecodeState(2, T * B + 5, g * hkv, hkv, d, chunk=B, alpha=alpha, gamma=3.0, page_size=B, num_pages=2,
+                         page_table=torch.arange(2, dtype=torch.int32).view(2, 1).repeat(1, slots))
+    st.kbar.copy_(torch.from_numpy(rng.standard_normal((2, hkv, T, d))))
+    for t in (st.k_codes, st.v_codes):
+        t.random_(0, 256)
+    st.k_scales.fill_(0x38)
+    st.v_scales.fill_(0x38)
+    st.seqlens.copy_(torch.tensor([T * B + 3, T * B - 1], dtype=torch.int32))
+    q = torch.from_numpy(rng.standard_normal((2, g * hkv, d))).bfloat16().cuda()
+    clean = st.decode(q).clone()
+    assert torch.isfinite(clean).all()
+    st.kbar[0, 1, T - 2, 7] = bad
+    st.kbar[0, 1, T - 2, 9] = -bad
+    rt = _routes(st, 2)
+    o = st.decode(q).clone()
+    assert torch.isnan(o[0, g:]).all()
+    assert torch.equal(o[0, :g], clean[0, :g]) and torch.equal(o[1], clean[1])
+    n = int(rt[0][0, 1])
+    assert T - 2 in rt[1][0, 1, :n].tolist() and torch.isnan(rt[2][0, 1, :n]).all()
+    # a query that is not a number stays in its head
+    st.kbar[0, 1, T - 2, 7] = st.kbar[0, 1, T - 2, 9] = 0.0
+    q[1, 1, 3] = bad
+    o = st.decode(q)
+    assert torch.isnan(o[1, 1]).all() and torch.isfinite(o[1, 0]).all() and torch.isfinite(o[1, 2:]).all()
+    assert torch.isfinite(o[0]).all()
