@@ -95,6 +95,7 @@ class Q4DecodeState:
         self.workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=self.device)
         self._ws_bytes = self.workspace.shape[0]
         self.route = None
+        self._recorded = None   # graph_step: graph, inputs, tensors and descriptions it was recorded with
 
     @property
     def qbar(self):
@@ -226,20 +227,26 @@ class Q4DecodeState:
     def graph_step(self, q, k_new, v_new):
         """step() through a CUDA graph: the first call runs eagerly and records append + decode on
         static input buffers; later calls copy the inputs in and replay (lengths and page table are
-        read on the device, so one graph serves every step)."""
-        if getattr(self, "_graph", None) is None:
+        read on the device, so one graph serves every step).  A call that finds qbar, route or another
+        of the tensors and descriptions that a step takes its addresses from replaced does as the first."""
+        takes = (self._qbar, self.kbar, self.state, self.seqlens, self.O, self.workspace)
+        described = (bytes(self.p), bytes(self.kv), None if self.route is None else bytes(self.route))
+        got = self._recorded
+        if got is None or got[3] != described or any(a is not b for a, b in zip(got[2], takes)):
             out = self.step(q, k_new, v_new)
-            self._ins = [t.clone(memory_format=torch.contiguous_format) for t in (q, k_new, v_new)]
-            self._graph = torch.cuda.CUDAGraph()
-            with torch.cuda.device(self.device), torch.cuda.graph(self._graph):
-                self.step(*self._ins)
+            ins = [t.clone(memory_format=torch.contiguous_format) for t in (q, k_new, v_new)]
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.device(self.device), torch.cuda.graph(graph):
+                self.step(*ins)
+            self._recorded = graph, ins, takes, described   # (the graph keeps what it takes alive)
             return out
-        for mine, t in zip(self._ins, (q, k_new, v_new)):
+        graph, ins = got[:2]
+        for mine, t in zip(ins, (q, k_new, v_new)):
             if t.shape != mine.shape or t.dtype != mine.dtype:
                 raise ValueError(f"the graph was recorded for {mine.dtype} {tuple(mine.shape)}")
-        for mine, t in zip(self._ins, (q, k_new, v_new)):
+        for mine, t in zip(ins, (q, k_new, v_new)):
             mine.copy_(t)
-        self._graph.replay()
+        graph.replay()
         return self.O
 
 
