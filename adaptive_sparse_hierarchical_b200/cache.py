@@ -37,6 +37,12 @@ def _need(t, name, device, dtype, shape=None):
     return t
 
 
+def _table(t, batch):
+    """t as a page table of `batch` rows: the kernels follow that many rows' entries."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[0] < batch:
+        raise ValueError(f"page_table: a row [max_pages] for each of the {batch} sequences is needed")
+
+
 def _int32(v, name):
     """A number that a C int holds (anything else would be cut down silently)."""
     if not -2**31 <= v < 2**31:
@@ -68,6 +74,7 @@ class Q4DecodeState:
             page_table = torch.arange(batch * slots, dtype=torch.int32).view(batch, slots)
         if num_pages is None:
             num_pages = batch * slots
+        _table(page_table, batch)
         self.page_table = page_table.to(device=device, dtype=torch.int32).contiguous()
         self.device = self.page_table.device
         self._index = self.device.index
