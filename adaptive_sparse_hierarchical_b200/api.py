@@ -175,6 +175,13 @@ class DecodeState:
         self._graph.replay()
         return self.O
 
+
+def _table(t, batch):
+    """t as a page table of `batch` rows: the kernels follow that many rows' entries."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[0] < batch:
+        raise ValueError(f"page_table: a row [max_pages] for each of the {batch} sequences is needed")
+
+
 class PagedDecodeState:
     """DecodeState on paged K/V pools [num_pages, page_size, h_kv, d] with a page table
     [batch, max_pages] (device int32) that the caller may rewrite between steps; the summary
@@ -182,6 +189,7 @@ class PagedDecodeState:
 
     def __init__(self, batch, capacity, h_q, h_kv, d, *, chunk, alpha, gamma, page_size, num_pages,
                  page_table, inv_sigma=1.0, device="cuda", qbar=None):
+        _table(page_table, batch)
         self.K = torch.zeros((num_pages, page_size, h_kv, d), dtype=torch.bfloat16, device=device)
         self.V = torch.zeros_like(self.K)
         self.page_table = page_table.to(device=device, dtype=torch.int32).contiguous()

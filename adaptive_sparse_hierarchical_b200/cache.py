@@ -6,7 +6,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib as L
-from .api import _st
+from .api import _st, _table
 
 
 def _current(index):
@@ -35,12 +35,6 @@ def _need(t, name, device, dtype, shape=None):
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(shape)} is needed, not {tuple(t.shape)}")
     return t
-
-
-def _table(t, batch):
-    """t as a page table of `batch` rows: the kernels follow that many rows' entries."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[0] < batch:
-        raise ValueError(f"page_table: a row [max_pages] for each of the {batch} sequences is needed")
 
 
 def _int32(v, name):
