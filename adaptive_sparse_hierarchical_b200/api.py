@@ -208,11 +208,19 @@ class PagedDecodeState:
         ws = L.dash_workspace_size(self.p, L.DASH_OP_DECODE)
         self.workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=device)
         self.route = None
+        self._held = None   # refs and status of the PagePool that the cache belongs to
 
     def fill(self, K0, V0, lengths, stream=None):
         """Copy the first lengths[b] prefilled keys/values of K0, V0 [b, L0, h_kv, d] into the
-        sequences' pages and build the summary cache (Eq. 4)."""
+        sequences' pages and build the summary cache (Eq. 4).  Refused where a PagePool counts another
+        row on one of those pages."""
         pt = self.page_table.cpu()
+        if self._held is not None:
+            refs = self._held[0].cpu()
+            for b in range(K0.shape[0]):
+                for pid in pt[b, :(int(lengths[b]) + self.page_size - 1) // self.page_size].tolist():
+                    if 0 <= pid < refs.shape[0] and refs[pid] > 1:
+                        raise ValueError(f"sequence {b}: page {pid} is held by another row too")
         for b in range(K0.shape[0]):
             n = int(lengths[b])
             for j in range((n + self.page_size - 1) // self.page_size):

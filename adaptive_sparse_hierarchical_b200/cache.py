@@ -58,7 +58,8 @@ class Q4DecodeState:
     k_exp, v_exp: power-of-two exponents of the data's size (scales cover 2^-9 .. 448 times 2^exp).
     page_table (device int32 [batch, max_pages]) may be rewritten between steps, by the caller or by
     a PagePool; without one, sequence b owns pages b * max_pages and on.  Copying the tensors saves
-    or restores a session.  Calls share the cache's workspace and output, so they go to one stream at
+    or restores a session.  Tokens are written from seqlens on: a row whose pages another row shares
+    is not to be moved back by hand.  Calls share the cache's workspace and output, so they go to one stream at
     a time (graphs of one cache are replayed one after another)."""
 
     def __init__(self, batch, capacity, h_q, h_kv, d, *, chunk, alpha, gamma, page_size, num_pages=None,
@@ -96,6 +97,7 @@ class Q4DecodeState:
         self.workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=self.device)
         self._ws_bytes = self.workspace.shape[0]
         self.route = None
+        self._held = None       # refs and status of the PagePool that the cache belongs to
         self._recorded = None   # graph_step: graph, inputs, tensors and descriptions it was recorded with
 
     @property
@@ -163,11 +165,24 @@ class Q4DecodeState:
             L._check(rc, "dash_append_q4")
 
     def fill(self, K0, V0, lengths, stream=None):
-        """Start over with the first lengths[b] tokens of K0, V0 [batch, n, h_kv, d]."""
+        """Start over with the first lengths[b] tokens of K0, V0 [batch, n, h_kv, d], in the pages that the
+        table holds.  Where a PagePool counts another row on one of those pages, nothing changes and the
+        pool's check() tells (free the rows first, and reserve their pages anew)."""
         with _within(self.device, stream):
             lengths = torch.as_tensor(lengths, dtype=torch.int32).to(self.device).contiguous()
-            self._check("append", K0, V0, lengths, "lengths")
-            self.seqlens.zero_()
+            _, n = self._check("append", K0, V0, lengths, "lengths")
+            if self._held is None:
+                self.seqlens.zero_()
+            else:
+                refs, status = self._held
+                ends = (lengths.clamp(0, min(n, self._shape["seqlen"])) + (self.page_size - 1)) // self.page_size
+                table = self.page_table[:lengths.shape[0]]
+                written = torch.arange(table.shape[1], device=self.device) < ends[:, None]
+                pages = torch.where(written & (table >= 0) & (table < refs.shape[0]), table, -1).long()
+                shared = ((pages >= 0) & (refs[pages.clamp(min=0)] > 1)).any()
+                status.copy_(torch.where(shared & (status == 0), PagePool.SHARED, status))
+                self.seqlens.mul_(shared)
+                lengths = lengths * ~shared
             self.append(K0, V0, lengths)
 
     def load(self, start, n, K=None, V=None, stream=None):
@@ -261,7 +276,9 @@ class PagePool:
     one stream at a time."""
 
     REASONS = {1: "an index is outside its range, or a page is missing", 2: "a destination occurs twice or is also a source",
-               3: "a destination row is not empty", 4: "not enough free pages", 5: "a length is beyond the row's pages"}
+               3: "a destination row is not empty", 4: "not enough free pages", 5: "a length is beyond the row's pages",
+               6: "a page to be filled is held by another row too"}
+    SHARED = 6   # (set by the caches' fill; the others are the library's)
 
     def __init__(self, page_table, refs, seqlens, *, page_size):
         self.device = page_table.device
@@ -316,6 +333,7 @@ class PagePool:
                                                        s.shape[1], 1, 0, L.DASH_ROW_STATE))
         if state.seqlens.data_ptr() != self.seqlens.data_ptr():
             self.add_rows(state.seqlens, clear=True)
+        state._held = self.refs, self.status   # fill asks them
 
     def add_pages(self, t):
         """Register a pool tensor [num_pages, ...] with contiguous pages."""

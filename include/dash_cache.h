@@ -44,7 +44,8 @@ typedef struct {
  * L_b = seqlens[b] and on, in 4 bits; the summaries (Eq. 4) are taken from the bf16 keys: every
  * chunk they complete is written to kbar_cache, the chunk they leave open to partial_state (the
  * buffers of dash_summary_append; the state is not read while L_b is a multiple of the chunk).
- * seqlens[b] becomes L_b + counts[b].  Tokens beyond the capacity p->seqlen are dropped. */
+ * seqlens[b] becomes L_b + counts[b].  Tokens beyond the capacity p->seqlen are dropped.  (Rows that share pages
+ * share filled ones: a caller that sets seqlens[b] back below them would write what the other row reads.) */
 int dash_append_q4(const dash_params* p, const dash_q4_kv* kv, const void* K_new, const void* V_new, int n_new,
                    const int* counts, const float* qbar, float* kbar_cache, float* partial_state, int* seqlens,
                    void* stream);

@@ -84,3 +84,92 @@ def test_a_recording_that_fails_leaves_no_graph(monkeypatch):
     graph.graph_step(*b)
     assert torch.equal(graph.graph_step(*b), want)
     _same_state(eager, graph)
+
+
+@pytest.mark.parametrize("layers", [1, 2])
+def test_fill_spares_pages_that_rows_share(layers):
+    """After a fork, fill would write the prompt into pages that another row reads: it changes nothing and check()
+    tells why; with the rows freed and pages given out anew it runs, into pages of its own."""
+    rnd = _rnd(4)
+    table = torch.full((4, 8), -1, dtype=torch.int32, device="cuda")
+    sts = [_make(4, num_pages=20, page_table=table) for _ in range(layers)]
+    pool = D.PagePool.of(sts)
+    K, V, q = rnd(4, 200, HKV, DIM), rnd(4, 200, HKV, DIM), rnd(4, HQ, DIM)
+    lens = _ints(200, 70, 0, 0)
+    pool.reserve(lens)
+    for st in sts:
+        st.fill(K, V, lens)
+        st.fill(V, K, lens)       # (nothing is shared yet)
+        st.fill(K, V, lens)
+    pool.fork([0], [3])
+    pool.check()
+    before = [[t.clone() for t in (st.k_codes, st.v_codes, st.k_scales, st.v_scales, st.kbar, st.state, st.seqlens)] for st in sts]
+    out = [st.decode(q).clone() for st in sts]
+    for k, st in enumerate(sts):
+        for bad in ([150, 0, 0, 0], _ints(0, 0, 0, 150), [200, 70, 0, 200]):
+            st.fill(V, K, bad)
+            for x, y in zip(before[k], (st.k_codes, st.v_codes, st.k_scales, st.v_scales, st.kbar, st.state, st.seqlens)):
+                assert torch.equal(x, y)
+            with pytest.raises(D.DashError, match="another row"):
+                pool.check()
+        assert torch.equal(st.decode(q), out[k])
+    pool.free([0, 1])             # row 3 now holds its pages alone
+    pool.reserve(_ints(130, 0, 64, 0))
+    free = _ints(130, 0, 64, 0)
+    for k, st in enumerate(sts):
+        st.append(V[:, :130], K[:, :130], free)
+        assert torch.equal(st.decode(q)[3], out[k][3])
+    pool.check()
+    for st in sts:
+        st.fill(K, V, [100, 0, 10, 150])   # every page has one holder: the caches start over
+        assert st.seqlens.tolist() == [100, 0, 10, 150]
+    pool.check()
+
+
+def test_fill_of_shared_pages_in_a_graph():
+    """The check runs on the device: a captured fill spares shared pages at every replay."""
+    rnd = _rnd(5)
+    table = torch.full((3, 8), -1, dtype=torch.int32, device="cuda")
+    st = _make(3, num_pages=20, page_table=table)
+    pool = D.PagePool.of([st])
+    K, V, lens = rnd(3, 128, HKV, DIM), rnd(3, 128, HKV, DIM), _ints(128, 0, 0)
+    pool.reserve(lens)
+    st.fill(K, V, lens)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        st.fill(V, K, lens)
+    graph.replay()
+    swapped = st.k_codes.clone()
+    st.fill(K, V, lens)
+    held = st.k_codes.clone()
+    assert not torch.equal(held, swapped)
+    pool.fork([0], [1])
+    graph.replay()
+    assert torch.equal(st.k_codes, held) and st.seqlens.tolist() == [128, 128, 0]
+    with pytest.raises(D.DashError, match="another row"):
+        pool.check()
+    pool.free([1])
+    graph.replay()
+    assert torch.equal(st.k_codes, swapped)
+    pool.check()
+
+
+def test_fill_of_a_bf16_cache_spares_shared_pages():
+    rnd = _rnd(6)
+    table = torch.full((3, 4), -1, dtype=torch.int32, device="cuda")
+    st = D.PagedDecodeState(3, 256, HQ, HKV, 128, chunk=64, alpha=1.5, gamma=3.0, page_size=PAGE, num_pages=10, page_table=table,
+                            qbar=torch.zeros(HKV, 128, device="cuda"))
+    pool = D.PagePool.of([st])
+    K, V = rnd(3, 150, HKV, 128), rnd(3, 150, HKV, 128)
+    pool.reserve(_ints(150, 0, 60))
+    st.fill(K, V, [150, 0, 60])
+    st.fill(K, V, [150, 0, 60])
+    pool.fork([0], [1])
+    before = [t.clone() for t in (st.K, st.V, st.kbar, st.state, st.seqlens)]
+    with pytest.raises(ValueError, match="another row"):
+        st.fill(V, K, [150, 0, 60])
+    for x, y in zip(before, (st.K, st.V, st.kbar, st.state, st.seqlens)):
+        assert torch.equal(x, y)
+    pool.free([1])
+    st.fill(V, K, [150, 0, 60])
+    assert torch.equal(st.K[int(table[0, 0])], V[0, :PAGE])
