@@ -98,7 +98,7 @@ class Q4DecodeState:
         self._ws_bytes = self.workspace.shape[0]
         self.route = None
         self._held = None       # refs and status of the PagePool that the cache belongs to
-        self._recorded = None   # graph_step: graph, inputs, tensors and descriptions it was recorded with
+        self._recorded = {}     # graph_step, by the number of inputs: graph, inputs, what it was recorded with
 
     @property
     def qbar(self):
@@ -236,31 +236,37 @@ class Q4DecodeState:
             L._check(rc, "dash_decode_q4")
         return self.O
 
-    def step(self, q, k_new, v_new, stream=None):
-        self.append(k_new, v_new, stream=stream)
+    def step(self, q, k_new, v_new, stream=None, counts=None):
+        """append(k_new, v_new, counts), then decode(q): rows whose count is 0 take no token (and need
+        no page for it); their outputs are those of their last token."""
+        self.append(k_new, v_new, counts, stream)
         return self.decode(q, stream)
 
-    def graph_step(self, q, k_new, v_new):
+    def graph_step(self, q, k_new, v_new, counts=None):
         """step() through a CUDA graph: the first call runs eagerly and records append + decode on
         static input buffers; later calls copy the inputs in and replay (lengths and page table are
-        read on the device, so one graph serves every step).  A call that finds qbar, route or another
-        of the tensors and descriptions that a step takes its addresses from replaced does as the first."""
+        read on the device, so one graph serves every step, and one more every step with counts).  A
+        call that finds qbar, route or another of the tensors and descriptions that a step takes its
+        addresses from replaced does as the first."""
         takes = (self._qbar, self.kbar, self.state, self.seqlens, self.O, self.workspace)
         described = (bytes(self.p), bytes(self.kv), None if self.route is None else bytes(self.route))
-        got = self._recorded
+        args = (q, k_new, v_new) if counts is None else (q, k_new, v_new, counts)
+        got = self._recorded.get(len(args))
         if got is None or got[3] != described or any(a is not b for a, b in zip(got[2], takes)):
-            out = self.step(q, k_new, v_new)
-            ins = [t.clone(memory_format=torch.contiguous_format) for t in (q, k_new, v_new)]
+            out = self.step(q, k_new, v_new, counts=counts)
+            ins = [t.clone(memory_format=torch.contiguous_format) for t in args]
             graph = torch.cuda.CUDAGraph()
             with torch.cuda.device(self.device), torch.cuda.graph(graph):
-                self.step(*ins)
-            self._recorded = graph, ins, takes, described   # (the graph keeps what it takes alive)
+                self.step(*ins[:3], counts=None if counts is None else ins[3])
+            self._recorded[len(args)] = graph, ins, takes, described   # (the graph keeps what it takes alive)
             return out
         graph, ins = got[:2]
-        for mine, t in zip(ins, (q, k_new, v_new)):
+        if counts is not None:
+            self._rows(counts, "counts")
+        for mine, t in zip(ins, args):
             if t.shape != mine.shape or t.dtype != mine.dtype:
                 raise ValueError(f"the graph was recorded for {mine.dtype} {tuple(mine.shape)}")
-        for mine, t in zip(ins, (q, k_new, v_new)):
+        for mine, t in zip(ins, args):
             mine.copy_(t)
         graph.replay()
         return self.O

@@ -173,3 +173,66 @@ def test_fill_of_a_bf16_cache_spares_shared_pages():
     pool.free([1])
     st.fill(V, K, [150, 0, 60])
     assert torch.equal(st.K[int(table[0, 0])], V[0, :PAGE])
+
+
+def test_rows_that_take_no_token():
+    """step and graph_step with counts: rows with 0 keep their length, pages and state, an emptied row can be forked
+    into, and both equal append(counts) + decode."""
+    rnd = _rnd(7)
+    made = []
+    for _ in range(3):
+        table = torch.full((4, 8), -1, dtype=torch.int32, device="cuda")
+        st = _make(4, num_pages=24, page_table=table)
+        made.append((st, D.PagePool.of([st])))
+    K, V = rnd(4, 120, HKV, DIM), rnd(4, 120, HKV, DIM)
+    for st, pool in made:
+        pool.reserve(_ints(120, 60, 5, 0))
+        st.fill(K, V, [120, 60, 5, 0])
+        pool.free([1])
+    stream = torch.cuda.Stream()
+    on = [1, 0, 1, 0]
+    lens = [120, 0, 5, 0]
+    for t in range(75):
+        if t == 40:
+            for _, pool in made:
+                pool.fork([0], [3])
+                pool.check()
+            on, lens[3] = [1, 0, 0, 1], lens[0]
+        counts = _ints(*on)
+        lens = [n + c for n, c in zip(lens, on)]
+        ins = _step(rnd, 4)
+        outs = []
+        for k, (st, pool) in enumerate(made):
+            pool.reserve(counts)
+            if k == 0:
+                st.append(ins[1], ins[2], counts)
+                outs.append(st.decode(ins[0]).clone())
+            elif k == 1:
+                outs.append(st.graph_step(*ins, counts=counts).clone())
+            else:
+                stream.wait_stream(torch.cuda.current_stream())
+                o = st.step(*ins, counts=counts, stream=stream)
+                torch.cuda.current_stream().wait_stream(stream)
+                outs.append(o.clone())
+            pool.check()
+            assert st.seqlens.tolist() == lens and (pool.page_table[1] == -1).all()
+        assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2]) and not outs[0][1].any()
+    for st, _ in made[1:]:
+        _same_state(made[0][0], st)
+
+
+def test_recorded_steps_with_and_without_counts():
+    """One cache's recorded steps of both kinds in turn equal the eager ones; counts of another size are refused."""
+    rnd = _rnd(8)
+    eager, graph = _make(), _make()
+    for t in range(12):
+        ins, counts = _step(rnd), _ints(t % 2, 1, t % 3) if t % 4 < 2 else None
+        assert torch.equal(eager.step(*ins, counts=counts).clone(), graph.graph_step(*ins, counts=counts))
+    _same_state(eager, graph)
+    ins, lens = _step(rnd), graph.seqlens.tolist()
+    for bad in (_ints(1, 1), _ints(1, 1, 1).long(), torch.tensor([1, 1, 1], dtype=torch.int32)):
+        with pytest.raises((TypeError, ValueError)):
+            graph.graph_step(*ins, counts=bad)
+        with pytest.raises((TypeError, ValueError)):
+            graph.step(*ins, counts=bad)
+    assert graph.seqlens.tolist() == lens
