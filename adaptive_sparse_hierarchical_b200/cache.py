@@ -220,15 +220,18 @@ class Q4DecodeState:
             L._check(rc, "dash_load_q4")
         return K, V
 
+    def _query(self, q):
+        if _signature(q) != self._seen.get("q"):
+            if not _need(q, "q", self.device, torch.bfloat16, self.O.shape).is_contiguous():
+                raise ValueError("q must be contiguous")
+            self._seen["q"] = _signature(q)
+
     def decode(self, q, stream=None):
         """Attention of the query q [batch, h_q, d] of each sequence's last token; zeros for an empty one."""
         if _elsewhere(self._index, stream):
             with _within(self.device, stream):
                 return self.decode(q)
-        if _signature(q) != self._seen.get("q"):
-            if not _need(q, "q", self.device, torch.bfloat16, self.O.shape).is_contiguous():
-                raise ValueError("q must be contiguous")
-            self._seen["q"] = _signature(q)
+        self._query(q)
         rc = self._lib.dash_decode_q4(self.p, self.kv, q.data_ptr(), self.kbar.data_ptr(), self.seqlens.data_ptr(),
                                       self.O.data_ptr(), self.route, self.workspace.data_ptr(), self._ws_bytes,
                                       _current(self._index))
@@ -239,6 +242,9 @@ class Q4DecodeState:
     def step(self, q, k_new, v_new, stream=None, counts=None):
         """append(k_new, v_new, counts), then decode(q): rows whose count is 0 take no token (and need
         no page for it); their outputs are those of their last token."""
+        self._query(q)   # a query that decode would refuse: nothing is appended
+        if q.data_ptr() % 16:
+            raise L.DashError("dash_decode_q4: q must be 16-byte aligned")
         self.append(k_new, v_new, counts, stream)
         return self.decode(q, stream)
 

@@ -236,3 +236,20 @@ def test_recorded_steps_with_and_without_counts():
         with pytest.raises((TypeError, ValueError)):
             graph.step(*ins, counts=bad)
     assert graph.seqlens.tolist() == lens
+
+
+def test_a_step_that_is_refused_appends_nothing():
+    rnd = _rnd(9)
+    st = _make()
+    q, k, v = _step(rnd)
+    st.step(q, k, v)
+    held = st.k_codes.clone()
+    for bad in (q.float(), q[:2], q[:, :4], q.cpu(), q.transpose(0, 1).contiguous().transpose(0, 1), None):
+        with pytest.raises((TypeError, ValueError)):
+            st.step(bad, k, v)
+        with pytest.raises((TypeError, ValueError)):
+            st.graph_step(bad, k, v)
+    off = torch.zeros(3 * HQ * DIM + 4, dtype=torch.bfloat16, device="cuda")[4:].view(3, HQ, DIM)   # 8 bytes past the alignment
+    with pytest.raises(D.DashError):
+        st.step(off, k, v)
+    assert st.seqlens.tolist() == [1, 1, 1] and torch.equal(st.k_codes, held)
