@@ -155,6 +155,9 @@ class Q4DecodeState:
             with _within(self.device, stream):
                 return self.append(k_new, v_new, counts)
         p, n = self._check("append", k_new, v_new, counts, "counts")
+        self._append(p, n, k_new, v_new, counts)
+
+    def _append(self, p, n, k_new, v_new, counts):
         q = self._qbar
         if q is None:
             raise TypeError("qbar is needed")
@@ -170,7 +173,8 @@ class Q4DecodeState:
         pool's check() tells (free the rows first, and reserve their pages anew)."""
         with _within(self.device, stream):
             lengths = torch.as_tensor(lengths, dtype=torch.int32).to(self.device).contiguous()
-            _, n = self._check("append", K0, V0, lengths, "lengths")
+            p, n = self._check("append", K0, V0, lengths, "lengths")
+            self._append(p, 0, K0, V0, lengths)   # no tokens: the library's checks, before anything changes
             if self._held is None:
                 self.seqlens.zero_()
             else:
@@ -183,7 +187,7 @@ class Q4DecodeState:
                 status.copy_(torch.where(shared & (status == 0), PagePool.SHARED, status))
                 self.seqlens.mul_(shared)
                 lengths = lengths * ~shared
-            self.append(K0, V0, lengths)
+            self._append(p, n, K0, V0, lengths)
 
     def load(self, start, n, K=None, V=None, stream=None):
         """Positions start[b] .. start[b] + n - 1 (start: a number or device int32 [batch]) in bf16:

@@ -253,3 +253,21 @@ def test_a_step_that_is_refused_appends_nothing():
     with pytest.raises(D.DashError):
         st.step(off, k, v)
     assert st.seqlens.tolist() == [1, 1, 1] and torch.equal(st.k_codes, held)
+
+
+def test_a_fill_that_is_refused_changes_nothing():
+    rnd = _rnd(10)
+    st = _make()
+    K = rnd(3, 40, HKV, DIM)
+    st.fill(K, K, [40, 3, 0])
+    wide = torch.zeros(3, 40, HKV, DIM + 4, dtype=torch.bfloat16, device="cuda")[..., :DIM]   # rows 136 bytes apart
+    with pytest.raises(D.DashError):
+        st.fill(wide, K, [40, 3, 1])
+    qbar, st.qbar = st.qbar, None
+    with pytest.raises(TypeError):
+        st.fill(K, K, [40, 3, 1])
+    st.qbar = qbar
+    for bad in ([1, 2], [[1, 2, 3]]):
+        with pytest.raises((TypeError, ValueError)):
+            st.fill(K, K, bad)
+    assert st.seqlens.tolist() == [40, 3, 0]
