@@ -459,8 +459,11 @@ class PagePool:
         return self.used
 
     def check(self):
-        """Raise DashError if an operation since the last check could not be carried out (synchronises)."""
+        """Raise DashError if an operation since the last check could not be carried out, on whichever
+        stream it went (waits for the device)."""
+        torch.cuda.synchronize(self.device)
         code = int(self.status.item())
         if code:
             self.status.zero_()
+            torch.cuda.synchronize(self.device)   # later operations, on any stream, find it cleared
             raise L.DashError(f"page operation: {self.REASONS.get(code, code)}")

@@ -271,3 +271,18 @@ def test_a_fill_that_is_refused_changes_nothing():
         with pytest.raises((TypeError, ValueError)):
             st.fill(K, K, bad)
     assert st.seqlens.tolist() == [40, 3, 0]
+
+
+def test_check_sees_operations_on_other_streams():
+    """check() waits for operations wherever they were enqueued, and what it clears stays apart from later ones."""
+    table = torch.full((2, 4), -1, dtype=torch.int32, device="cuda")
+    pool = D.PagePool(table, torch.zeros(8, dtype=torch.int32, device="cuda"), _ints(0, 0), page_size=PAGE)
+    stream = torch.cuda.Stream()
+    for _ in range(3):
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            torch.cuda._sleep(20_000_000)   # some 10 ms
+        pool.reserve(10000, stream=stream)
+        with pytest.raises(D.DashError, match="length"):
+            pool.check()
+        pool.check()
