@@ -28,6 +28,7 @@ constexpr int kMove = 256;              // threads of a mover block
 constexpr long long kPiece = 16ll * kMove;
 constexpr int kSlots = 1024;            // table entries it takes at a time
 constexpr int kFew = 256;               // a list short enough for every block to check
+constexpr int kHeld = 16;               // table entries of a fork's destination that a lane looks at per step
 constexpr int kMarks = 4096;            // rows whose marks fit a plan's shared memory
 
 // Workspace header, then the lists (see PagesWs).
@@ -266,9 +267,23 @@ __global__ void __launch_bounds__(kPlan) plan_fork_kernel(PageTab t, const int* 
     if (on && inside) {
         mark[d] = i;
         L = t.seqlens[s];
-        const int Ld = t.seqlens[d], held = t.page_table[(long long)d * t.max_pages];
         if (L < 0 || L > (long long)t.max_pages * t.page_size) bad |= 1u << DASH_PAGES_LENGTH;
-        else if (Ld != 0 || held >= 0) bad |= 1u << DASH_PAGES_BUSY;
+        else if (t.seqlens[d] != 0) bad |= 1u << DASH_PAGES_BUSY;
+    }
+    // no slot of a destination may hold a page: a warp per entry, kHeld slots of a lane on their way at a time
+    for (int j = threadIdx.x >> 5; j < n; j += kPlan / 32) {
+        const int to = dst[j];
+        if (to < 0 || to >= t.batch) continue;
+        const int* row = t.page_table + (long long)to * t.max_pages;
+        int top = -1;
+        for (int s0 = threadIdx.x & 31; s0 < t.max_pages; s0 += 32 * kHeld) {
+            int e[kHeld];
+#pragma unroll
+            for (int k = 0; k < kHeld; ++k) e[k] = s0 + 32 * k < t.max_pages ? row[s0 + 32 * k] : -1;
+#pragma unroll
+            for (int k = 0; k < kHeld; ++k) top = max(top, e[k]);
+        }
+        if (top >= 0) bad |= 1u << DASH_PAGES_BUSY;
     }
     int code = first_failure(bad, status), want = 0, at = 0, part = 0;
     if (!code) {

@@ -286,3 +286,49 @@ def test_check_sees_operations_on_other_streams():
         with pytest.raises(D.DashError, match="length"):
             pool.check()
         pool.check()
+
+
+def test_fork_into_a_row_that_holds_any_page():
+    """A row of length 0 whose first slot is empty but a later one is not is not empty: its pages are not lost."""
+    for slots, at in ((4, 2), (40, 39), (1500, 1499), (1500, 33)):
+        table = torch.full((3, slots), -1, dtype=torch.int32, device="cuda")
+        refs = torch.zeros(8, dtype=torch.int32, device="cuda")
+        table[0, 0], table[1, at] = 5, 3
+        refs[5] = refs[3] = 1
+        lens = _ints(20, 0, 0)
+        pool = D.PagePool(table, refs, lens, page_size=PAGE)
+        before = table.clone(), refs.clone(), lens.clone()
+        pool.fork([0, 0], [2, 1])
+        for x, y in zip(before, (table, refs, lens)):
+            assert torch.equal(x, y)
+        with pytest.raises(D.DashError, match="not empty"):
+            pool.check()
+        pool.free([1])
+        pool.fork([0, 0], [2, 1])
+        pool.check()
+        assert refs.tolist() == [1, 1, 0, 0, 0, 1, 0, 0] and lens.tolist() == [20, 20, 20]
+
+
+def test_fork_many_rows_of_many_slots():
+    """More entries than the check takes at a time, full tables beside them."""
+    rows, slots = 900, 70
+    table = torch.full((rows, slots), -1, dtype=torch.int32, device="cuda")
+    refs = torch.zeros(200, dtype=torch.int32, device="cuda")
+    table[:2] = torch.arange(2 * slots, dtype=torch.int32, device="cuda").view(2, slots)
+    refs[: 2 * slots] = 1
+    lens = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    lens[:2] = slots * PAGE
+    pool = D.PagePool(table, refs, lens, page_size=PAGE)
+    src = torch.arange(rows - 2, device="cuda").int() % 2
+    dst = torch.arange(2, rows, device="cuda").int()
+    table[700, 69] = 150
+    refs[150] = 1
+    before = table.clone(), refs.clone()
+    pool.fork(src, dst)
+    with pytest.raises(D.DashError, match="not empty"):
+        pool.check()
+    assert torch.equal(before[0], table) and torch.equal(before[1], refs)
+    pool.free([700])
+    pool.fork(src, dst)
+    pool.check()
+    assert torch.equal(table[2:], table[:2][src.long()]) and refs[: 2 * slots].tolist() == [450] * (2 * slots)
