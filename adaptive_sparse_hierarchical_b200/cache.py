@@ -415,7 +415,8 @@ class PagePool:
         self._pair(self._lib.dash_pages_copy, "dash_pages_copy", src, dst)
 
     def reserve(self, count=1, stream=None):
-        """Give rows the pages they lack for `count` more tokens (a number, or device int32 [batch])."""
+        """Give rows the pages they lack for their next `count` tokens (a number, or device int32 [batch]);
+        slots before the next token's are left as they are."""
         if _elsewhere(self._index, stream):
             with _within(self.device, stream):
                 return self.reserve(count)

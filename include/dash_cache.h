@@ -119,8 +119,10 @@ size_t dash_pages_workspace_size(const dash_pages* pg);
 int dash_pages_copy(const dash_pages* pg, const int* src, const int* dst, int n, int* status, void* workspace,
                     size_t ws_bytes, void* stream);
 
-/* Gives every row b the free pages it lacks for positions up to seqlens[b] + add_b - 1, add_b =
- * counts ? counts[b] : count (rows with add_b <= 0 are left alone). */
+/* Gives every row b the free pages it lacks for positions seqlens[b] .. seqlens[b] + add_b - 1, add_b =
+ * counts ? counts[b] : count (rows with add_b <= 0 are left alone).  Slots before the one of position
+ * seqlens[b] stay as they are: where one is unmapped its tokens were not stored, and a page given to it now
+ * would put what the page held before in their place. */
 int dash_pages_reserve(const dash_pages* pg, const int* counts, int count, int* status, void* workspace,
                        size_t ws_bytes, void* stream);
 

@@ -332,3 +332,21 @@ def test_fork_many_rows_of_many_slots():
     pool.fork(src, dst)
     pool.check()
     assert torch.equal(table[2:], table[:2][src.long()]) and refs[: 2 * slots].tolist() == [450] * (2 * slots)
+
+
+def test_reserve_looks_from_the_next_token_on():
+    """Slots before the one of the next token are left as they are: what a row without a page there dropped reads as
+    zeros, not as what a page held before."""
+    rnd = _rnd(11)
+    table = torch.full((2, 8), -1, dtype=torch.int32, device="cuda")
+    st = _make(2, num_pages=12, page_table=table)
+    pool = D.PagePool.of([st])
+    for t in (st.k_codes, st.v_codes, st.k_scales, st.v_scales):
+        t.fill_(0x31)   # what other rows left there
+    K = rnd(2, 2 * PAGE, HKV, DIM)
+    pool.reserve(_ints(PAGE, PAGE))
+    st.append(K, K, _ints(2 * PAGE, PAGE))   # row 0 has no page for its second half
+    pool.reserve(_ints(5, 5))
+    pool.check()
+    assert (table[0] >= 0).tolist() == [True, False, True] + [False] * 5 and (table[1, :2] >= 0).all()
+    assert not st.load(PAGE, PAGE)[0][0].any()
