@@ -139,7 +139,8 @@ class Q4DecodeState:
             if k4.shape[1] != v4.shape[1]:
                 raise ValueError("K and V hold different numbers of tokens")
             self._rows(rows, name)
-            got = self._remember(key, (L.params(**s, k_strides=_st(k4), v_strides=_st(v4)), k4.shape[1]))
+            n = _int32(k4.shape[1], "tokens")
+            got = self._remember(key, (L.params(**s, k_strides=_st(k4), v_strides=_st(v4)), n))
         return got
 
     def _remember(self, key, value):

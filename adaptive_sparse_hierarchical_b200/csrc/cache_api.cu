@@ -183,6 +183,7 @@ int dash_load_q4(const dash_params* p, const dash_q4_kv* kv, const int* start, i
     if (!on(K, 16) || !on(V, 16) || !rows_ok(p->k_strides) || !rows_ok(p->v_strides)) return DASH_EALIGN;
     if (!on(start, 4) || !on(seqlens, 4)) return DASH_EALIGN;
     if (n == 0) return DASH_OK;
+    if (n > 1 << 30) return DASH_EUNSUPPORTED;   // the blocks' rows are numbered in 32 bits, the last block's spare ones too
     if (!apart(p, p->k_strides, n) || !apart(p, p->v_strides, n)) return DASH_EINVAL;
     return status_of(launch_load_q4(shape_of(p), cache_of(kv), start, offset, n, seqlens, K, V, (cudaStream_t)stream));
 }

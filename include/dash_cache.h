@@ -52,7 +52,7 @@ int dash_append_q4(const dash_params* p, const dash_q4_kv* kv, const void* K_new
 
 /* Read back: K, V [batch, n, h_kv, d_h] (bf16, strides p->k_strides / p->v_strides) receive
  * positions start_b .. start_b + n - 1 of every sequence, start_b = (start ? start[b] : 0) +
- * offset.  Positions outside 0..seqlens[b]-1 or on unmapped pages give zeros. */
+ * offset.  Positions outside 0..seqlens[b]-1 or on unmapped pages give zeros.  n <= 2^30. */
 int dash_load_q4(const dash_params* p, const dash_q4_kv* kv, const int* start, int offset, int n, const int* seqlens,
                  void* K, void* V, void* stream);
 

@@ -39,3 +39,19 @@ def test_page_tables_of_other_shapes_bf16(table):
         make(table)
     for rows in (4, 6):
         assert make(torch.zeros(rows, 9, dtype=torch.int32)).pk.max_pages == 9
+
+
+def test_token_numbers_beyond_32_bits():
+    """The rows of load are numbered in 32 bits with the last block's spare ones, and a C int holds the number."""
+    lib, i = D.load(), 256
+    p = D.params(batch=1, seqlen=512, h_q=4, h_kv=2, d_h=64, chunk=32, alpha=1.5, gamma=2.0, k_strides=(1 << 40, 128, 64),
+                 v_strides=(1 << 40, 128, 64))
+    pool = torch.zeros(8, 2, 64, 32, dtype=torch.uint8)
+    kv = D.q4_kv(pool, pool[..., :2].contiguous(), pool, pool[..., :2].contiguous(), torch.zeros(1, 8, dtype=torch.int32), page_size=64)
+    for n in ((1 << 31) - 1, (1 << 30) + 1):
+        assert lib.dash_load_q4(p, kv, None, 0, n, i, i, i, None) == -2   # DASH_EUNSUPPORTED
+    st = _q4(qbar=torch.zeros(2, 64))
+    many = torch.zeros(64, dtype=torch.bfloat16).expand(4, (1 << 32) + 1, 2, 64)
+    for call in (lambda: st._check("append", many, many, None, "counts"), lambda: st._check("load", many, many, None, "start")):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
