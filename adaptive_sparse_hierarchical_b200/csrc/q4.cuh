@@ -16,13 +16,30 @@ struct Q4 {
     int kexp, vexp;
 };
 
+// An entry of the page table: an ordinary load (the kernel ahead may have been writing the table when this one started,
+// which rules the read-only path out), but one that the compiler may place freely.  That is safe because nobody writes
+// the table once the kernel ahead has ended, and `p` has to depend on a length read after that (as it does wherever a
+// token's number is checked against one).
+__device__ __forceinline__ int table_entry(const int* p)
+{
+    int v;
+    asm("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(__cvta_generic_to_global(p)));
+    return v;
+}
+
 // Page of token t of sequence b, or -1 where none is mapped.
-__device__ __forceinline__ int q4_page(const Q4& c, int b, int t)
+template <typename F>
+__device__ __forceinline__ int q4_page(const Q4& c, int b, int t, F entry)
 {
     const int slot = t / c.psz;
     if (t < 0 || slot >= c.pmax) return -1;
-    const int pg = __ldg(c.pt + (long long)b * c.pmax + slot);
+    const int pg = entry(c.pt + (long long)b * c.pmax + slot);
     return pg >= 0 && pg < c.npages ? pg : -1;
+}
+
+__device__ __forceinline__ int q4_page(const Q4& c, int b, int t)
+{
+    return q4_page(c, b, t, [](const int* e) { return table_entry(e); });
 }
 
 // Two e4m3 bytes (low byte first) as f16x2; exact, the code 0x7f gives a NaN.

@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(32 * kLoadWarps) load_kernel(Shape s, Q4 c, Lo
             ++slot;
             in -= c.psz;
         }
-        const int pg = slot < c.pmax ? __ldg(table + slot) : -1;
+        const int pg = slot < c.pmax ? table_entry(table + slot) : -1;
         if (pg < 0 || pg >= c.npages) continue;
         const long long row = (long long)r * c.psz + in;
         kw[u] = *reinterpret_cast<const uint32_t*>(c.kc + pg * c.kcp + row * (D / 2) + key_word<D>(sub) * 4);

@@ -34,9 +34,8 @@ constexpr int kCl = 4, kThr = 512, kWarps = kThr / 32, kMaxVals = 32, kLong = 8;
 
 // X [pair][head][T]: the logits of the complete chunks before each query's own.
 template <int D>
-__global__ void __launch_bounds__(32 * kLogitWarps) route_logits_kernel(Shape s, const __nv_bfloat16* __restrict__ q,
-                                                                        const float* __restrict__ kbar,
-                                                                        const int* __restrict__ seqlens, float* X)
+__global__ void __launch_bounds__(32 * kLogitWarps) route_logits_kernel(Shape s, const __nv_bfloat16* q, const float* kbar,
+                                                                        const int* seqlens, float* X)
 {
     pdl_wait();   // the append of this step
     pdl_launch_dependents();
@@ -88,7 +87,7 @@ __host__ __device__ inline int quarter(int nv) { return ((nv + kCl - 1) / kCl + 
 // Thresholds: a block per (pair, head).  The head's weights [x - tau]_+^p take its logits' place in X.  V: entries per
 // thread, held in registers; 0: rows of any length, read again (from L1 and L2) at every step, kLong at a time.
 template <int V>
-__global__ void __launch_bounds__(kThr) route_tau_kernel(Shape s, float* X, const int* __restrict__ seqlens, int* status)
+__global__ void __launch_bounds__(kThr) route_tau_kernel(Shape s, float* X, const int* seqlens, int* status)
 {
     __shared__ float red[kWarps];
     __shared__ float2 part[2][kWarps];
@@ -166,7 +165,7 @@ __global__ void __launch_bounds__(kThr) route_tau_kernel(Shape s, float* X, cons
 
 // Group weights and lists: a cluster of 4 blocks per pair, a quarter of the chunks each.
 __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThr, 1)
-    route_list_kernel(Shape s, const float* X, const int* __restrict__ seqlens, Routes rt)
+    route_list_kernel(Shape s, const float* X, const int* seqlens, Routes rt)
 {
     extern __shared__ float keep[];   // the weights of this block's quarter of the chunks
     __shared__ float lsum[kWarps];
@@ -253,9 +252,8 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThr, 1)
 }
 
 template <int D, int V>
-__global__ void __launch_bounds__(512) route_short_kernel(Shape s, const __nv_bfloat16* __restrict__ q,
-                                                          const float* __restrict__ kbar, const int* __restrict__ seqlens,
-                                                          Routes rt, int* status)
+__global__ void __launch_bounds__(512) route_short_kernel(Shape s, const __nv_bfloat16* q, const float* kbar,
+                                                          const int* seqlens, Routes rt, int* status)
 {
     __shared__ float x[16 * (32 * V + 4)], sums_of[2 * V];
     pdl_wait();   // the append of this step

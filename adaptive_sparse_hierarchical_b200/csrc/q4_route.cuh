@@ -29,8 +29,8 @@ __device__ __forceinline__ void load_tile(float2 (&u)[D / 16][2], const float* p
 {
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-        u[kk][0] = on ? __ldg(reinterpret_cast<const float2*>(p + kk * 16)) : make_float2(0.f, 0.f);
-        u[kk][1] = on ? __ldg(reinterpret_cast<const float2*>(p + kk * 16 + 8)) : make_float2(0.f, 0.f);
+        u[kk][0] = on ? *reinterpret_cast<const float2*>(p + kk * 16) : make_float2(0.f, 0.f);
+        u[kk][1] = on ? *reinterpret_cast<const float2*>(p + kk * 16 + 8) : make_float2(0.f, 0.f);
     }
 }
 // acc += q u^T: heads g8 and g8 + 8, chunks 2 t4 and 2 t4 + 1

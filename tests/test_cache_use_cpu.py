@@ -1,4 +1,7 @@
 """Refusals of the cache classes that need no GPU: nothing is launched."""
+import os
+import re
+
 import pytest
 import torch
 
@@ -55,3 +58,16 @@ def test_token_numbers_beyond_32_bits():
     for call in (lambda: st._check("append", many, many, None, "counts"), lambda: st._check("load", many, many, None, "start")):
         with pytest.raises(ValueError, match="32 bits"):
             call()
+
+
+def test_no_read_only_loads_of_what_a_running_kernel_may_write():
+    """The cache's kernels start before the one ahead of them ends (programmatic dependent launch).  What that one writes
+    (tables, lengths, summaries, logits) may then not be read by the read-only path, which holds only for memory
+    that nobody writes while the kernel runs: neither __ldg nor const __restrict__ pointers."""
+    src = os.path.join(os.path.dirname(D.__file__), "csrc")
+    for name in ("q4.cuh", "q4_cache.cu", "q4_decode.cu", "q4_route.cuh", "q4_route.cu", "pages.cuh", "pages.cu"):
+        text = open(os.path.join(src, name)).read()
+        text = re.sub(r"//[^\n]*", "", text)
+        # (the page table, where the routing's launches lie between the kernel and whoever wrote it)
+        text = text.replace("!SOLO && !a.dense ? __ldg(e) : table_entry(e)", "", 1)
+        assert not re.findall(r"__ldg|__restrict__|ld\.global\.nc", text), name
