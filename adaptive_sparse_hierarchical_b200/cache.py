@@ -342,14 +342,23 @@ class PagePool:
             raise ValueError("the cache must have been made with this pool's page table and page size")
         pools = [state.k_codes, state.k_scales, state.v_codes, state.v_scales] if isinstance(state, Q4DecodeState) \
             else [state.K, state.V]
-        for t in pools:
-            self.add_pages(t)
-        self.add_rows(state.kbar, unit_tokens=state.p.chunk)
         s = state.state
-        self._register(s, self._rows, L.dash_row_array(s.data_ptr(), s.stride(0) * 4, s.stride(1) * 4, s.shape[2] * 4,
-                                                       s.shape[1], 1, 0, L.DASH_ROW_STATE))
-        if state.seqlens.data_ptr() != self.seqlens.data_ptr():
-            self.add_rows(state.seqlens, clear=True)
+        if s.stride(2) != 1:
+            raise ValueError("the incomplete-chunk state must be contiguous")
+        before = len(self._arrays), len(self._rows), len(self._kept)
+        try:
+            for t in pools:
+                self.add_pages(t)
+            self.add_rows(state.kbar, unit_tokens=state.p.chunk)
+            self._register(s, self._rows, L.dash_row_array(s.data_ptr(), s.stride(0) * 4, s.stride(1) * 4, s.shape[2] * 4,
+                                                           s.shape[1], 1, 0, L.DASH_ROW_STATE))
+            if state.seqlens.data_ptr() != self.seqlens.data_ptr():
+                self.add_rows(state.seqlens, clear=True)
+        except ValueError:   # all of a cache or nothing of it
+            for kept, n in zip((self._arrays, self._rows, self._kept), before):
+                del kept[n:]
+            self._describe()
+            raise
         state._held = self.refs, self.status   # fill asks them
 
     def add_pages(self, t):

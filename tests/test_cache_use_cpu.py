@@ -71,3 +71,20 @@ def test_no_read_only_loads_of_what_a_running_kernel_may_write():
         # (the page table, where the routing's launches lie between the kernel and whoever wrote it)
         text = text.replace("!SOLO && !a.dense ? __ldg(e) : table_entry(e)", "", 1)
         assert not re.findall(r"__ldg|__restrict__|ld\.global\.nc", text), name
+
+
+@pytest.mark.parametrize("name", ["k_scales", "v_codes", "kbar", "state"])
+def test_a_cache_that_is_refused_is_not_registered_in_part(name):
+    """add of a cache one of whose tensors is refused registers none of them; put right, it is registered once."""
+    table = torch.full((4, 8), -1, dtype=torch.int32)
+    st, other = _q4(page_table=table), _q4(page_table=table)
+    pool = D.PagePool.of([st])
+    arrays, rows = pool.pg.num_arrays, pool.pg.num_rows
+    right = getattr(other, name)
+    setattr(other, name, right.repeat_interleave(2, -1)[..., ::2])   # the same values, not contiguous
+    with pytest.raises(ValueError):
+        pool.add(other)
+    assert (pool.pg.num_arrays, pool.pg.num_rows) == (arrays, rows)
+    setattr(other, name, right)
+    pool.add(other)
+    assert (pool.pg.num_arrays, pool.pg.num_rows) == (2 * arrays, 2 * rows + 1)
