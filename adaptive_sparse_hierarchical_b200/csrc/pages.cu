@@ -10,8 +10,9 @@
 // launch).  A copy of at most kFew pages needs no plan: every mover block checks the list itself.
 //
 // Measured: 1111 pages of 65.5 KB in each of 8 pools, 1.16 GB read and written: 188 us, 6.2 TB/s (a copy kernel
-// reaches 6.5).  Compaction of 8192 pages, half of them in use (537 MB): 98.7 us, of which the plan is 8.  32
-// children of 8 rows of 32K tokens (84 MB): 25 us.  Three pages: 6.1 us, the call itself.  The plans are one
+// reaches 6.5).  Compaction of 8192 pages, half of them in use (537 MB): 98.7 us, of which the plan is 8.  Pools of 4
+// bits have pages of 16 KB (codes) and 1 KB (scales), less than a piece: 2.9 to 3.3 TB/s.  32 children of 8 rows of 32K
+// tokens (84 MB): 26 us.  Three pages: 5.9 us, the call itself.  The plans are one
 // block's work: reserving 131072 tokens for each of 64 rows (65536 slots) takes 0.32 ms, freeing them (a block
 // per row) 18 us; a decode step's reserve finds its few slots in one step of the block.
 #include "q4.cuh"

@@ -28,9 +28,9 @@
 //      8 times the sum of P s, kept by one more MMA for two groups (A = the scales, B = P).
 //   P is rounded to f16 (2^-12 relative; sums of P are taken before the rounding, in fp32), turned from S^T's
 //   accumulator layout into an operand by movmatrix, and P s is rounded to f16 once more (2^-12, of terms with codes
-//   up to 15).  P is 2^room at the reference, and both P and P s stay below 2^15: room is 9 while the value scales
-//   met so far are below 1/2, less for larger ones (0 from 256 on), so small scales do not push P s below f16's
-//   normals.  The reference moves only when a logit exceeds it by more than 6, or when room shrinks.
+//   up to 15).  P is 2^room at the reference and at most 2^(room + 6), and P s stays below 2^15: room is 9 while the
+//   value scales s met so far are below 1, then 8 - floor(log2 s) of the largest (0 from 256 on), so small scales do not
+//   push P s below f16's normals.  The reference moves only when a logit exceeds room by more than 6, or when room shrinks.
 //
 // Bound: 17/32 bytes of HBM per element are few enough for the unpacking to count: per 16 tokens of 128
 // elements and 8 heads a warp issues some 260 instructions, of them 56 masks, 16 shifts and permutations, 14
@@ -38,8 +38,8 @@
 // Measured (L2 flushed): 48 pairs of 50021 tokens and fewer, 8 heads, all of it 283 MB: 60 us a call in short runs
 // (4.7 TB/s, 72% of a copy; 58% of the issue slots, 56% of the integer pipe's and 34% of the tensor pipe's
 // cycles), 64 to 66 in long ones, where the GPU's 1000 W hold the clock at 1.8 GHz.  A kernel without its loads takes
-// 2 us less: it is the instructions.  16 pairs of 131072 tokens, 16 heads, a quarter routed, 91 MB: 35.6 us of a
-// call's 54.4, some 7 of them the start and the merge.  Three sequences of 777 tokens and fewer, routed: 7.8 us a
+// 2 us less: it is the instructions.  16 pairs of 131072 tokens, 16 heads, a quarter routed, 91 MB: 36 us of a
+// call's 54.8, some 7 of them the start and the merge.  Three sequences of 777 tokens and fewer, routed: 7.8 us a
 // call, one launch.
 // The values' scales on the weights' side instead of in every operand, with rows of one group per tile: 2% with
 // the copies as they were, 8% with what it made possible (the byte permutation, two conversions at once).  No

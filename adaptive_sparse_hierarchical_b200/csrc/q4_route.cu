@@ -9,8 +9,9 @@
 // and has every head's threshold solved on a list that crosses blocks.  Here
 //   1. a warp takes 16 chunks of a pair, reads their summaries once (all loads in flight together) and
 //      writes the group's logits: HBM-bound, 4 d bytes per chunk;
-//   2. a block per (pair, head) holds the head's row in registers: a Newton step is one pass over them and one
-//      block barrier.  The weights take the logits' place (in L2);
+//   2. a block per (pair, head) holds the head's row in registers, less its maximum: a Newton step is one pass over them
+//      and one block barrier.  The weights take the logits' place (in L2).  Rows of more than 16384 chunks are read again
+//      at every step instead (one pair of 57600 chunks: 55 us a call);
 //   3. in a cluster of 4 blocks per pair each block adds up the heads' weights for a quarter of the chunks, and
 //      the blocks tell each other their counts and sums of logarithms.
 // Short rows take one block and one launch instead (route_short_kernel; in the shortest caches the attending block
