@@ -354,7 +354,7 @@ class PagePool:
                                                            s.shape[1], 1, 0, L.DASH_ROW_STATE))
             if state.seqlens.data_ptr() != self.seqlens.data_ptr():
                 self.add_rows(state.seqlens, clear=True)
-        except ValueError:   # all of a cache or nothing of it
+        except Exception:   # all of a cache or nothing of it
             for kept, n in zip((self._arrays, self._rows, self._kept), before):
                 del kept[n:]
             self._describe()

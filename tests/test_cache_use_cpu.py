@@ -86,5 +86,10 @@ def test_a_cache_that_is_refused_is_not_registered_in_part(name):
         pool.add(other)
     assert (pool.pg.num_arrays, pool.pg.num_rows) == (arrays, rows)
     setattr(other, name, right)
+    seqlens, other.seqlens = other.seqlens, None   # not a tensor at all
+    with pytest.raises(AttributeError):
+        pool.add(other)
+    assert (pool.pg.num_arrays, pool.pg.num_rows) == (arrays, rows)
+    other.seqlens = seqlens
     pool.add(other)
     assert (pool.pg.num_arrays, pool.pg.num_rows) == (2 * arrays, 2 * rows + 1)
